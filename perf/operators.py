@@ -246,13 +246,13 @@ def _bits(flags):
 
 def _q4_weights(packed, scale, zero, group):
     """The (k, n) matrix in 32 bits.  Word j of lane 4 g + t of tile (tn, tk) holds channels 16 tn + g + 8 c and
-    inputs 64 tk + 16 t + 4 j + i, i = 0..3, at bits 4 c + 8 (i / 2) + 16 (i % 2)."""
+    inputs 64 tk + 32 (j / 2) + 8 t + 4 (j % 2) + i, i = 0..3, at bits 4 c + 8 (i / 2) + 16 (i % 2)."""
     tn, tk = packed.shape[:2]
-    w = packed.view(tn, tk, 8, 4, 4, 1, 1)
+    w = packed.view(tn, tk, 8, 4, 2, 2, 1, 1)
     c = torch.arange(2, device=w.device, dtype=torch.int32).view(2, 1)
     i = torch.arange(4, device=w.device, dtype=torch.int32)
-    q = (w >> (4 * c + 8 * (i // 2) + 16 * (i % 2))) & 15          # tn, tk, g, t, j, c, i
-    q = q.permute(1, 3, 4, 6, 0, 5, 2).reshape(64 * tk, 16 * tn).float()
+    q = (w >> (4 * c + 8 * (i // 2) + 16 * (i % 2))) & 15          # tn, tk, g, t, j / 2, j % 2, c, i
+    q = q.permute(1, 4, 3, 5, 7, 0, 6, 2).reshape(64 * tk, 16 * tn).float()
     z = zero.float().repeat_interleave(group, 0)
     return (q - z) * scale.float().repeat_interleave(group, 0)
 
@@ -483,7 +483,7 @@ def _exact_q4(case, st):
         for field in range(8):
             low, c = field % 4, field % 2
             i = 2 * (low // 2) + field // 4
-            rows = 64 * tk.view(1, -1, 1) + 16 * (lane % 4) + 4 * j + i
+            rows = 64 * tk.view(1, -1, 1) + 32 * (j // 2) + 8 * (lane % 4) + 4 * (j % 2) + i
             cols = 16 * tn.view(-1, 1, 1) + lane // 4 + 8 * c
             w[rows, cols] = ((words[:, :, :, j] >> (4 * field)) % 16).double()
     for a in range(k // case["group"]):
