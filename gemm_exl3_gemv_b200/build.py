@@ -7,6 +7,7 @@ there.  nvcc cross-compiles, so no GPU is needed to build.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -43,14 +44,37 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+# object files, one per source and variant (git-ignored)
+OBJ_DIR = os.path.join(HERE, "_build")
+
+
 def _compile(lib: str, extra, verbose: bool):
+    """Compile every source whose object is older than it or any header, side
+    by side, and link the shared library."""
     nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, *FLAGS, *extra, "-shared", "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
+    tag = os.path.splitext(os.path.basename(lib))[0]
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    headers = [p for p in _inputs() + [os.path.abspath(__file__)] if not p.endswith(".cu")]
+    newest = max(os.path.getmtime(p) for p in headers)
+    flags = [*ARCH, *FLAGS, *extra, "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+        flags.append("-Xptxas=-v")
+
+    def compile_one(src):
+        obj = os.path.join(OBJ_DIR, f"{tag}_{os.path.splitext(os.path.basename(src))[0]}.o")
+        if verbose or not os.path.exists(obj) or os.path.getmtime(obj) < max(newest, os.path.getmtime(src)):
+            tmp = f"{obj}.tmp{os.getpid()}"
+            cmd = [nvcc, *flags, "-c", "-o", tmp, src]
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.run(cmd, check=True)
+            os.replace(tmp, obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count()) as pool:
+        objects = list(pool.map(compile_one, sources()))
+    tmp = lib + f".tmp{os.getpid()}"
+    subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objects], check=True)
     os.replace(tmp, lib)
 
 
