@@ -104,6 +104,8 @@ const char* exl3_status_string(int status)
         case EXL3_ERR_ARCH: return "EXL3_ERR_ARCH: current device is not a compute capability 10.0 GPU";
         case EXL3_ERR_CUDA: return "EXL3_ERR_CUDA: a CUDA runtime call failed (see exl3_last_cuda_error)";
         case EXL3_ERR_TIMEOUT: return "EXL3_ERR_TIMEOUT: a kernel gave up a bounded wait; output invalid";
+        case EXL3_ERR_CACHE_FULL: return "EXL3_ERR_CACHE_FULL: the cache has too few free pages or table entries";
+        case EXL3_ERR_INDEX: return "EXL3_ERR_INDEX: bad or repeated index in a list or in the cache's bookkeeping";
         case EXL3_ERR_BOUNDS: return "EXL3_ERR_BOUNDS: a debug-build index check failed; output invalid";
     }
     return "EXL3: unknown status";
@@ -384,4 +386,239 @@ extern "C" int exl3_gemv_noalloc(const uint16_t* x, const uint32_t* packed, cons
     a.pdl = 0;                       // follows a memset: ordinary stream order
     e = exl3::launch_gemv_m1(a, s);
     return e == cudaSuccess ? EXL3_OK : cuda_fail(e);
+}
+
+// --------------------------------------------------- 4-bit group products ---
+
+namespace {
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+bool q4_shape_ok(int k_in, int n_out)
+{
+    return k_in % 64 == 0 && k_in <= (1 << 20) && n_out % 16 == 0 && n_out <= 128 * exl3::kMaxBlocks;
+}
+
+}  // namespace
+
+extern "C" size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out)
+{
+    if (m <= 0 || m > 32 || k_in <= 0 || n_out <= 0 || !q4_shape_ok(k_in, n_out)) return 0;
+    return exl3::q4_workspace_bytes(m, k_in, n_out);
+}
+
+extern "C" int exl3_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,
+                            const uint8_t* zero, void* y, int y_fp32, int k_in, int n_out, int group,
+                            void* workspace, size_t ws_bytes, void* stream)
+{
+    if (!x || !packed || !scale || !y || m <= 0 || k_in <= 0 || n_out <= 0) return EXL3_ERR_INVALID_ARG;
+    if (m > 32 || !q4_shape_ok(k_in, n_out) || (group != 32 && group != 64 && group != 128) || k_in % group)
+        return EXL3_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(packed) || !aligned16(scale) || !aligned16(zero) || !aligned16(y))
+        return EXL3_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < exl3_q4_workspace_bytes(m, k_in, n_out)) return EXL3_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return EXL3_ERR_MISALIGNED;
+    const int st = check_arch();
+    if (st != EXL3_OK) return st;
+    const cudaError_t e = exl3::launch_q4_gemm(m, x, packed, scale, zero, y, y_fp32, k_in, n_out, group,
+                                               static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? EXL3_OK : cuda_fail(e);
+}
+
+extern "C" int exl3_q4_pack(const uint8_t* q, int k_in, int n_out, uint32_t* packed, void* stream)
+{
+    if (!q || !packed || k_in <= 0 || n_out <= 0) return EXL3_ERR_INVALID_ARG;
+    if (!q4_shape_ok(k_in, n_out)) return EXL3_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(packed)) return EXL3_ERR_MISALIGNED;
+    const int st = check_arch();
+    if (st != EXL3_OK) return st;
+    const cudaError_t e = exl3::launch_q4_pack(q, k_in, n_out, packed, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? EXL3_OK : cuda_fail(e);
+}
+
+// -------------------------------------------------- paged key-value cache ---
+
+namespace {
+
+// Validate a cache description and copy it into the kernels' form.
+int cache_args(const exl3_kv_cache_t* c, exl3::KvArgs& a)
+{
+    if (!c || !c->k || !c->v || !c->table || !c->lens || !c->refs || !c->free || !c->scratch) return EXL3_ERR_INVALID_ARG;
+    if (c->n_layers <= 0 || c->n_pages <= 0 || c->n_heads <= 0 || c->page_size <= 0 || c->head_dim <= 0 ||
+        c->n_seqs <= 0 || c->max_pages <= 0)
+        return EXL3_ERR_INVALID_ARG;
+    const int ps = c->page_size;
+    if ((c->head_dim != 64 && c->head_dim != 128) || (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) ||
+        c->n_heads > 256 || c->n_pages > (1 << 20) || c->n_seqs > 65536 || c->n_layers > 1024 ||
+        c->max_pages > (1 << 20) || (long long)c->max_pages * ps > (1ll << 30) ||
+        (long long)c->n_pages * c->n_heads * ps >= (1ll << 31))
+        return EXL3_ERR_UNSUPPORTED;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->table) || !aligned16(c->lens) || !aligned16(c->refs) ||
+        !aligned16(c->free) || !aligned16(c->scratch))
+        return EXL3_ERR_MISALIGNED;
+    a = exl3::KvArgs{c->k, c->v, c->table, c->lens, c->refs, c->free, static_cast<int*>(c->scratch), c->n_layers,
+                     c->n_pages, c->n_heads, ps, c->head_dim, c->n_seqs, c->max_pages};
+    return EXL3_OK;
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? EXL3_OK : cuda_fail(e); }
+
+// What every list call shares: the list's length, its pointers, the cache.
+int list_args(const exl3_kv_cache_t* c, int n, const int32_t* one, const int32_t* other, exl3::KvArgs& a)
+{
+    if (!one || n <= 0) return EXL3_ERR_INVALID_ARG;
+    if (n > exl3::kKvMaxList) return EXL3_ERR_UNSUPPORTED;
+    const int st = cache_args(c, a);
+    if (st != EXL3_OK) return st;
+    // lists are read number by number, so that a part of a list will do
+    if ((reinterpret_cast<uintptr_t>(one) | reinterpret_cast<uintptr_t>(other)) & 3u) return EXL3_ERR_MISALIGNED;
+    return EXL3_OK;
+}
+
+}  // namespace
+
+extern "C" size_t exl3_kv_scratch_bytes(int n_pages)
+{
+    return n_pages <= 0 || n_pages > (1 << 20) ? 0 : exl3::kv_scratch_bytes(n_pages);
+}
+
+extern "C" int exl3_kv_reset(const exl3_kv_cache_t* cache, void* stream)
+{
+    exl3::KvArgs a;
+    int st = cache_args(cache, a);
+    if (st == EXL3_OK) st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_reset(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int exl3_kv_status(const exl3_kv_cache_t* cache, void* stream)
+{
+    exl3::KvArgs a;
+    const int st = cache_args(cache, a);
+    if (st != EXL3_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, a.scratch + exl3::kKvFault, sizeof(word), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (word == 0) return EXL3_OK;
+    e = cudaMemsetAsync(a.scratch + exl3::kKvFault, 0, sizeof(word), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return (word & exl3::kKvIndex) ? EXL3_ERR_INDEX : EXL3_ERR_CACHE_FULL;
+}
+
+extern "C" int exl3_kv_extend(const exl3_kv_cache_t* cache, int n, int m, const int32_t* seqs, const int32_t* counts,
+                              void* stream)
+{
+    exl3::KvArgs a;
+    if (m <= 0) return EXL3_ERR_INVALID_ARG;
+    int st = list_args(cache, n, seqs, counts, a);
+    if (st == EXL3_OK) st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_extend(a, n, m, seqs, counts, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int exl3_kv_write(const exl3_kv_cache_t* cache, int layer, int n, int m, const int32_t* seqs,
+                             const int32_t* counts, const uint16_t* k_new, const uint16_t* v_new,
+                             long long batch_stride, long long row_stride, void* stream)
+{
+    exl3::KvArgs a;
+    if (!k_new || !v_new || m <= 0 || layer < 0 || batch_stride < 0 || row_stride < 0) return EXL3_ERR_INVALID_ARG;
+    int st = list_args(cache, n, seqs, counts, a);
+    if (st != EXL3_OK) return st;
+    if (layer >= a.n_layers) return EXL3_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || batch_stride % 8 || row_stride % 8) return EXL3_ERR_MISALIGNED;
+    st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_write(a, layer, n, m, seqs, counts, k_new, v_new, batch_stride, row_stride,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int exl3_kv_truncate(const exl3_kv_cache_t* cache, int n, const int32_t* seqs, const int32_t* new_lens,
+                                void* stream)
+{
+    exl3::KvArgs a;
+    int st = list_args(cache, n, seqs, new_lens, a);
+    if (st == EXL3_OK) st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_truncate(a, n, seqs, new_lens, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int exl3_kv_fork(const exl3_kv_cache_t* cache, int n, const int32_t* src, const int32_t* dst, void* stream)
+{
+    exl3::KvArgs a;
+    if (!dst) return EXL3_ERR_INVALID_ARG;
+    int st = list_args(cache, n, src, dst, a);
+    if (st == EXL3_OK) st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_fork(a, n, src, dst, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int exl3_kv_compact(const exl3_kv_cache_t* cache, void* stream)
+{
+    exl3::KvArgs a;
+    int st = cache_args(cache, a);
+    if (st == EXL3_OK) st = check_arch();
+    if (st != EXL3_OK) return st;
+    return cuda_status(exl3::launch_kv_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------- paged attention ---
+
+namespace {
+
+bool attention_heads_ok(int n_q_heads, int n_heads) { return n_q_heads % n_heads == 0 && n_q_heads / n_heads <= 32; }
+
+}  // namespace
+
+extern "C" size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim)
+{
+    if (m <= 0 || m > 32 || n_heads <= 0 || n_q_heads <= 0 || !attention_heads_ok(n_q_heads, n_heads) ||
+        (head_dim != 64 && head_dim != 128))
+        return 0;
+    return exl3::attention_workspace_bytes(m, n_q_heads, n_heads, head_dim);
+}
+
+extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int n, int m, const int32_t* seqs,
+                                    const int32_t* counts, const uint16_t* q, long long q_batch_stride,
+                                    long long q_row_stride, int n_q_heads, float scale, int window, int sinks,
+                                    uint16_t* out, long long out_batch_stride, long long out_row_stride, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream)
+{
+    exl3::AttnArgs t = {};
+    if (!q || !out || m <= 0 || n_q_heads <= 0 || layer < 0 || window < 0 || sinks < 0 || q_batch_stride < 0 ||
+        q_row_stride < 0 || out_batch_stride < 0 || out_row_stride < 0 || !(scale - scale == 0.f))
+        return EXL3_ERR_INVALID_ARG;
+    int st = list_args(cache, n, seqs, counts, t.c);
+    if (st != EXL3_OK) return st;
+    if (layer >= t.c.n_layers) return EXL3_ERR_INVALID_ARG;
+    if (m > 32 || !attention_heads_ok(n_q_heads, t.c.n_heads)) return EXL3_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || q_batch_stride % 8 || q_row_stride % 8 ||
+        out_batch_stride % 8 || out_row_stride % 8)
+        return EXL3_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < exl3_paged_attention_workspace_bytes(m, n_q_heads, t.c.n_heads, t.c.head_dim))
+        return EXL3_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return EXL3_ERR_MISALIGNED;
+    st = check_arch();
+    if (st != EXL3_OK) return st;
+    t.layer = layer;
+    t.n = n;
+    t.m = m;
+    t.seqs = seqs;
+    t.counts = counts;
+    t.q = q;
+    t.q_bs = q_batch_stride;
+    t.q_rs = q_row_stride;
+    t.n_q_heads = n_q_heads;
+    t.group = n_q_heads / t.c.n_heads;
+    t.scale = scale;
+    t.window = window;
+    t.sinks = sinks;
+    t.out = out;
+    t.o_bs = out_batch_stride;
+    t.o_rs = out_row_stride;
+    t.lse = lse;
+    t.ws = static_cast<unsigned char*>(workspace);
+    return cuda_status(exl3::launch_paged_attention(t, static_cast<cudaStream_t>(stream)));
 }

@@ -1,0 +1,453 @@
+// kv_cache.cu -- the bookkeeping and the data moves of a paged key-value cache
+// (exl3_kv_* in include/exl3.h): sequences grow, shrink, are forked and freed;
+// pages are allocated, copied and compacted; new keys and values are written.
+//
+// Everything is decided on the device, so that a decode step can be captured
+// in a graph.  Which pages are free is one bit each: 100,000 pages are 12.5 KB,
+// which a CTA counts through in one pass, and the lowest free page is the same
+// whatever the order of the atomics that freed it.  Calls that have to agree
+// on something (is the list good? do the pages suffice?) let every CTA work it
+// out for itself from data that no CTA of the call changes before the last one
+// has read it; no CTA waits for another.
+#include "exl3_common.cuh"
+#include "exl3_internal.h"
+
+namespace exl3 {
+
+namespace {
+
+__device__ __forceinline__ int pages_of(int tokens, int page_size) { return (tokens + page_size - 1) / page_size; }
+
+// Sum of v over the block's threads, and in `before` the sum over the threads
+// in front.  `tmp`: 33 ints of shared memory; ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ int block_scan(int v, int& before, int* tmp)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += o;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = s;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += tmp[w];
+        total += tmp[w];
+    }
+    before = base + s - v;
+    return total;
+}
+
+// Marks sequence s in the bitmap `seen`; false if it is out of range or marked
+// already.
+__device__ __forceinline__ bool mark(uint32_t* seen, int s, int n_seqs)
+{
+    if (s < 0 || s >= n_seqs) return false;
+    return (atomicOr(seen + (s >> 5), 1u << (s & 31)) >> (s & 31) & 1u) == 0;
+}
+
+__device__ __forceinline__ bool page_ok(const KvArgs& a, int p) { return p >= 0 && p < a.n_pages; }
+
+// One holder less of page p; the page is free after its last one.
+__device__ __forceinline__ void drop_page(const KvArgs& a, int p)
+{
+    if (atomicSub(a.refs + p, 1) == 1) atomicOr(a.free + (p >> 5), 1u << (p & 31));
+}
+
+__device__ __forceinline__ void fault(const KvArgs& a, int bits) { atomicOr(a.scratch + kKvFault, bits); }
+
+// ------------------------------------------------------------------ reset ---
+
+__global__ void __launch_bounds__(256) kv_reset_kernel(KvArgs a)
+{
+    grid_dep_wait();
+    const long long step = (long long)gridDim.x * blockDim.x, first = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    for (long long i = first; i < (long long)a.n_seqs * a.max_pages; i += step) a.table[i] = -1;
+    for (long long i = first; i < a.n_seqs; i += step) a.lens[i] = 0;
+    for (long long i = first; i < a.n_pages; i += step) a.refs[i] = 0;
+    for (long long i = first; i < (a.n_pages + 31) / 32; i += step) {
+        const int left = a.n_pages - 32 * (int)i;
+        a.free[i] = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+    }
+    for (long long i = first; i < kKvLists; i += step) a.scratch[i] = 0;
+}
+
+// ----------------------------------------------------------------- extend ---
+// grid (list entries, copiers).  Every CTA sums up what the whole list needs;
+// the CTAs of entry b take its pages, lowest first, from the free bits, and
+// share the copy of its last page if others hold that page too.  The table
+// entry of such a page, the lengths, the reference counts and the free bits
+// are what other CTAs still read: the last CTA to arrive writes them.
+
+constexpr int kExtThreads = 256;
+
+__global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n, int m, const int* seqs, const int* counts)
+{
+    extern __shared__ uint32_t seen[];                       // n_seqs bits
+    __shared__ int tmp[33];
+    __shared__ int copy_to, is_last;
+    const int tid = threadIdx.x, b = blockIdx.x, ps = a.page_size;
+    const int seen_words = (a.n_seqs + 31) / 32;
+    for (int i = tid; i < seen_words; i += kExtThreads) seen[i] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int old_fault = __ldcg(a.scratch + kKvFault);
+    __syncthreads();
+
+    // needs of this thread's entries (a contiguous run of the list)
+    const int per = (n + kExtThreads - 1) / kExtThreads;
+    const int e0 = min(n, tid * per), e1 = min(n, e0 + per);
+    int need = 0, bad = 0, my_need = 0, my_before = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int s = seqs[e], c = counts ? counts[e] : m;
+        if (!mark(seen, s, a.n_seqs) || c < 0 || c > m) { bad |= kKvIndex; continue; }
+        const int old = a.lens[s];
+        if (old < 0 || old > a.max_pages * ps) { bad |= kKvIndex; continue; }
+        if (c > a.max_pages * ps - old) { bad |= kKvFull; continue; }
+        int k = pages_of(old + c, ps) - pages_of(old, ps);
+        if (c > 0 && old % ps) {
+            const int p = a.table[(long long)s * a.max_pages + old / ps];
+            if (!page_ok(a, p)) { bad |= kKvIndex; continue; }
+            k += __ldcg(a.refs + p) > 1;
+        }
+        if (e == b) my_before = need, my_need = k;
+        need += k;
+    }
+    int before;
+    const int total = block_scan<kExtThreads>(need, before, tmp);
+    __shared__ int entry_before, entry_need;
+    if (b >= e0 && b < e1) { entry_before = before + my_before; entry_need = my_need; }
+    bad = __syncthreads_or(bad & kKvIndex) ? kKvIndex : __syncthreads_or(bad & kKvFull) ? kKvFull : 0;
+
+    // the free bits of this thread's words, and how many lie in front
+    const int words = (a.n_pages + 31) / 32, wper = (words + kExtThreads - 1) / kExtThreads;
+    const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
+    int free_before = 0;
+    if (!bad && total > 0) {
+        int have = 0;
+        for (int w = w0; w < w1; ++w) have += __popc(__ldcg(a.free + w));
+        const int all = block_scan<kExtThreads>(have, free_before, tmp);
+        if (total > all) bad = kKvFull;
+    }
+    if (bad || old_fault) {
+        if (bad && b == 0 && blockIdx.y == 0 && tid == 0) fault(a, bad);
+        return;                                              // the same answer in every CTA
+    }
+
+    const int s = seqs[b], c = counts ? counts[b] : m, old = a.lens[s];
+    const int first_new = pages_of(old, ps), fresh = pages_of(old + c, ps) - first_new;
+    const bool copy = entry_need > fresh;
+    if (entry_need > 0 && (blockIdx.y == 0 || copy)) {
+        const int r0 = entry_before, r1 = entry_before + entry_need;
+        int rank = free_before;
+        for (int w = w0; w < w1 && rank < r1; ++w) {
+            uint32_t bits = __ldcg(a.free + w);
+            const int k = __popc(bits);
+            if (rank + k <= r0) { rank += k; continue; }
+            for (; bits && rank < r1; bits &= bits - 1, ++rank) {
+                if (rank < r0) continue;
+                const int page = 32 * w + __ffs(bits) - 1, nth = rank - r0;
+                if (copy && nth == 0) {
+                    copy_to = page;
+                    if (blockIdx.y == 0) a.scratch[kKvCopy + b] = page;
+                } else if (blockIdx.y == 0) {
+                    a.table[(long long)s * a.max_pages + first_new + nth - (copy ? 1 : 0)] = page;
+                }
+            }
+        }
+    }
+    if (blockIdx.y == 0 && !copy && tid == 0) a.scratch[kKvCopy + b] = -1;
+    if (copy) {
+        __syncthreads();
+        // tokens of the shared page: per layer and head one run of old % ps rows
+        const int from = a.table[(long long)s * a.max_pages + old / ps], to = copy_to;
+        const int run = (old % ps) * a.head_dim / 8;         // 16-byte pieces
+        const long long page_vec = (long long)a.n_heads * ps * a.head_dim / 8, layer_vec = page_vec * a.n_pages;
+        const int runs = a.n_layers * a.n_heads;
+        for (int i = blockIdx.y; i < 2 * runs; i += gridDim.y) {
+            const int r = i >> 1, layer = r / a.n_heads, h = r % a.n_heads;
+            uint4* base = reinterpret_cast<uint4*>(i & 1 ? a.v : a.k) + layer * layer_vec + (long long)h * ps * a.head_dim / 8;
+            for (int x = tid; x < run; x += kExtThreads) base[to * page_vec + x] = base[from * page_vec + x];
+        }
+    }
+
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) is_last = atomicAdd(a.scratch + kKvArrived, 1) == (int)(gridDim.x * gridDim.y) - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    if (tid == 0) a.scratch[kKvArrived] = 0;
+    // the lowest `total` free pages are taken
+    int rank = free_before;
+    for (int w = w0; w < w1 && rank < total; ++w) {
+        uint32_t bits = __ldcg(a.free + w), take = 0;
+        for (; bits && rank < total; bits &= bits - 1, ++rank) {
+            take |= bits & -bits;
+            a.refs[32 * w + __ffs(bits) - 1] = 1;
+        }
+        if (take) atomicAnd(a.free + w, ~take);
+    }
+    __syncthreads();
+    for (int e = e0; e < e1; ++e) {
+        const int se = seqs[e], ce = counts ? counts[e] : m, oe = a.lens[se], to = __ldcg(a.scratch + kKvCopy + e);
+        if (to >= 0) {
+            int* slot = a.table + (long long)se * a.max_pages + oe / ps;
+            drop_page(a, *slot);
+            *slot = to;
+        }
+        a.lens[se] = oe + ce;
+    }
+}
+
+// ------------------------------------------------------------------ write ---
+// A thread moves 16 bytes of a key and of a value.  Bound by memory; what the
+// places cost (sequence, length, page: three dependent loads) is shared by the
+// 16 pieces of a row through the L1.
+
+__global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int n, int m, const int* seqs, const int* counts,
+                                                       const uint16_t* k_new, const uint16_t* v_new, long long bs,
+                                                       long long rs)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    if (__ldcg(a.scratch + kKvFault)) return;
+    const int row_vec = a.n_heads * a.head_dim / 8, head_vec = a.head_dim / 8, ps = a.page_size;
+    const long long all = (long long)n * m * row_vec;
+    const long long page_el = (long long)a.n_heads * ps * a.head_dim;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (long long)gridDim.x * blockDim.x) {
+        const int vec = (int)(i % row_vec);
+        const long long r = i / row_vec;
+        const int b = (int)(r / m), row = (int)(r % m);
+        const int c = counts ? counts[b] : m, s = seqs[b];
+        if (row >= c) continue;
+        if (c > m || s < 0 || s >= a.n_seqs) { fault(a, kKvIndex); continue; }
+        const int pos = a.lens[s] - c + row;
+        if (pos < 0 || pos >= a.max_pages * ps) { fault(a, kKvIndex); continue; }
+        const int page = a.table[(long long)s * a.max_pages + pos / ps];
+        if (!page_ok(a, page)) { fault(a, kKvIndex); continue; }
+        const long long to = ((long long)layer * a.n_pages + page) * page_el +
+                             ((long long)(vec / head_vec) * ps + pos % ps) * a.head_dim + 8 * (vec % head_vec);
+        const long long from = b * bs + row * rs + 8 * vec;
+        *reinterpret_cast<uint4*>(a.k + to) = *reinterpret_cast<const uint4*>(k_new + from);
+        *reinterpret_cast<uint4*>(a.v + to) = *reinterpret_cast<const uint4*>(v_new + from);
+    }
+}
+
+// --------------------------------------------------------- truncate, fork ---
+// One CTA per list entry; each checks the whole list (the lists are what no
+// CTA changes), then works on its own sequence's row alone.
+
+__global__ void __launch_bounds__(128) kv_truncate_kernel(KvArgs a, int n, const int* seqs, const int* new_lens)
+{
+    extern __shared__ uint32_t seen[];
+    const int words = (a.n_seqs + 31) / 32, ps = a.page_size;
+    for (int i = threadIdx.x; i < words; i += blockDim.x) seen[i] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    __syncthreads();
+    bool bad = false;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, seqs[e], a.n_seqs) || (new_lens && new_lens[e] < 0);
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) fault(a, kKvIndex);
+        return;
+    }
+    const int s = seqs[blockIdx.x];
+    const int old = min(max(a.lens[s], 0), a.max_pages * ps), now = min(old, new_lens ? new_lens[blockIdx.x] : 0);
+    int* row = a.table + (long long)s * a.max_pages;
+    for (int j = pages_of(now, ps) + threadIdx.x; j < pages_of(old, ps); j += blockDim.x) {
+        if (page_ok(a, row[j])) drop_page(a, row[j]);
+        else fault(a, kKvIndex);
+        row[j] = -1;
+    }
+    __syncthreads();                                         // the length was read by every thread
+    if (threadIdx.x == 0) a.lens[s] = now;
+}
+
+__global__ void __launch_bounds__(128) kv_fork_kernel(KvArgs a, int n, const int* src, const int* dst)
+{
+    extern __shared__ uint32_t seen[];
+    const int words = (a.n_seqs + 31) / 32, ps = a.page_size;
+    for (int i = threadIdx.x; i < words; i += blockDim.x) seen[i] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    __syncthreads();
+    bool bad = false;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, dst[e], a.n_seqs);
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+        const int s = src[e];
+        bad |= s < 0 || s >= a.n_seqs || (seen[s >> 5] >> (s & 31) & 1u);
+    }
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) fault(a, kKvIndex);
+        return;
+    }
+    const int s = src[blockIdx.x], d = dst[blockIdx.x];
+    const int len = min(max(a.lens[s], 0), a.max_pages * ps);
+    const bool taken = a.lens[d] != 0;
+    __syncthreads();                                         // before the new length is written
+    if (taken) {
+        if (threadIdx.x == 0) fault(a, kKvIndex);
+        return;
+    }
+    const int* from = a.table + (long long)s * a.max_pages;
+    int* to = a.table + (long long)d * a.max_pages;
+    for (int j = threadIdx.x; j < pages_of(len, ps); j += blockDim.x) {
+        const int p = from[j];
+        if (page_ok(a, p)) atomicAdd(a.refs + p, 1);
+        else fault(a, kKvIndex);
+        to[j] = p;
+    }
+    if (threadIdx.x == 0) a.lens[d] = len;
+}
+
+// ---------------------------------------------------------------- compact ---
+// Two launches: one CTA ranks the used pages behind the border and the free
+// ones before it; then the whole GPU moves the pages and renames them.  No
+// page is both a source and a destination, so the moves need no order.
+
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(KvArgs a)
+{
+    __shared__ int tmp[33];
+    grid_dep_wait();
+    const int tid = threadIdx.x, words = (a.n_pages + 31) / 32, per = (words + kPlanThreads - 1) / kPlanThreads;
+    const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    auto valid = [&](int w) { const int left = a.n_pages - 32 * w; return left >= 32 ? 0xffffffffu : (1u << left) - 1; };
+    int used = 0;
+    for (int w = w0; w < w1; ++w) used += __popc(~a.free[w] & valid(w));
+    int before;
+    const int border = block_scan<kPlanThreads>(used, before, tmp);
+    // free pages before the border, used pages behind it
+    auto below = [&](int w) { const int k = border - 32 * w; return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1; };
+    int holes = 0, strays = 0;
+    for (int w = w0; w < w1; ++w) {
+        const uint32_t f = a.free[w], lo = below(w);
+        holes += __popc(f & lo);
+        strays += __popc(~f & valid(w) & ~lo);
+    }
+    int hole_at, stray_at;
+    const int moves = block_scan<kPlanThreads>(holes, hole_at, tmp);
+    block_scan<kPlanThreads>(strays, stray_at, tmp);
+    int* src = a.scratch + kKvLists;
+    int* dst = src + (a.n_pages + 1) / 2;
+    for (int w = w0; w < w1; ++w) {
+        const uint32_t f = a.free[w], lo = below(w);
+        for (uint32_t x = f & lo; x; x &= x - 1) dst[hole_at++] = 32 * w + __ffs(x) - 1;
+        for (uint32_t x = ~f & valid(w) & ~lo; x; x &= x - 1) src[stray_at++] = 32 * w + __ffs(x) - 1;
+    }
+    __syncthreads();
+    int* name = src + (a.n_pages + 63) / 64 * 64;            // new ids of the pages behind the border
+    for (int i = tid; i < moves; i += kPlanThreads) name[src[i]] = dst[i];
+    if (tid == 0) {
+        a.scratch[kKvMoves] = moves;
+        a.scratch[kKvUsed] = border;
+    }
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMovePieces = 4;                               // 16-byte pieces in flight per thread
+
+__global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(KvArgs a)
+{
+    grid_dep_wait();
+    const int moves = a.scratch[kKvMoves], border = a.scratch[kKvUsed], ps = a.page_size;
+    if (moves == 0) return;
+    const int* src = a.scratch + kKvLists;
+    const int* dst = src + (a.n_pages + 1) / 2;
+    const int* name = src + (a.n_pages + 63) / 64 * 64;
+    const int page_vec = a.n_heads * ps * a.head_dim / 8;
+    constexpr int kChunk = kMoveThreads * kMovePieces;
+    const int chunks = (page_vec + kChunk - 1) / kChunk;
+    const long long items = (long long)moves * 2 * a.n_layers * chunks;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int chunk = (int)(it % chunks);
+        const long long r = it / chunks;
+        const int half = (int)(r & 1), layer = (int)((r >> 1) % a.n_layers), mv = (int)((r >> 1) / a.n_layers);
+        uint4* base = reinterpret_cast<uint4*>(half ? a.v : a.k) + (long long)layer * a.n_pages * page_vec;
+        const uint4* from = base + (long long)src[mv] * page_vec;
+        uint4* to = base + (long long)dst[mv] * page_vec;
+        uint4 buf[kMovePieces];
+        const int x0 = chunk * kChunk + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kMovePieces; ++i)
+            if (x0 + i * kMoveThreads < page_vec) buf[i] = from[x0 + i * kMoveThreads];
+#pragma unroll
+        for (int i = 0; i < kMovePieces; ++i)
+            if (x0 + i * kMoveThreads < page_vec) to[x0 + i * kMoveThreads] = buf[i];
+    }
+    const long long first = (long long)blockIdx.x * kMoveThreads + threadIdx.x, step = (long long)gridDim.x * kMoveThreads;
+    for (long long i = first; i < moves; i += step) {
+        a.refs[dst[i]] = a.refs[src[i]];
+        a.refs[src[i]] = 0;
+    }
+    for (long long i = first; i < (a.n_pages + 31) / 32; i += step) {
+        const int left = a.n_pages - 32 * (int)i, in = border - 32 * (int)i;
+        const uint32_t all = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+        const uint32_t taken = in >= 32 ? 0xffffffffu : in <= 0 ? 0u : (1u << in) - 1;
+        a.free[i] = all & ~taken;
+    }
+    const int warps = gridDim.x * (kMoveThreads / 32), lane = threadIdx.x & 31;
+    for (int s = (int)(first >> 5); s < a.n_seqs; s += warps) {
+        int* row = a.table + (long long)s * a.max_pages;
+        const int held = pages_of(min(max(a.lens[s], 0), a.max_pages * ps), ps);
+        for (int j = lane; j < held; j += 32) {
+            const int p = row[j];
+            if (!page_ok(a, p)) fault(a, kKvIndex);
+            else if (p >= border) row[j] = name[p];
+        }
+    }
+}
+
+size_t seen_bytes(const KvArgs& a) { return sizeof(uint32_t) * (size_t)((a.n_seqs + 31) / 32); }
+
+}  // namespace
+
+cudaError_t launch_kv_reset(const KvArgs& a, cudaStream_t stream)
+{
+    return launch_pdl(kv_reset_kernel, dim3(148), dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_kv_extend(const KvArgs& a, int n, int m, const int* seqs, const int* counts, cudaStream_t stream)
+{
+    int copiers = (148 + n - 1) / n;
+    if (copiers > 2 * a.n_layers * a.n_heads) copiers = 2 * a.n_layers * a.n_heads;
+    if (copiers > 16) copiers = 16;
+    return launch_pdl(kv_extend_kernel, dim3((unsigned)n, (unsigned)copiers), dim3(kExtThreads), seen_bytes(a), stream, a,
+                      n, m, seqs, counts);
+}
+
+cudaError_t launch_kv_write(const KvArgs& a, int layer, int n, int m, const int* seqs, const int* counts,
+                            const uint16_t* k_new, const uint16_t* v_new, long long batch_stride,
+                            long long row_stride, cudaStream_t stream)
+{
+    const long long pieces = (long long)n * m * a.n_heads * a.head_dim / 8, blocks = (pieces + 255) / 256;
+    return launch_pdl(kv_write_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)), dim3(256), 0, stream, a,
+                      layer, n, m, seqs, counts, k_new, v_new, batch_stride, row_stride);
+}
+
+cudaError_t launch_kv_truncate(const KvArgs& a, int n, const int* seqs, const int* new_lens, cudaStream_t stream)
+{
+    return launch_pdl(kv_truncate_kernel, dim3((unsigned)n), dim3(128), seen_bytes(a), stream, a, n, seqs, new_lens);
+}
+
+cudaError_t launch_kv_fork(const KvArgs& a, int n, const int* src, const int* dst, cudaStream_t stream)
+{
+    return launch_pdl(kv_fork_kernel, dim3((unsigned)n), dim3(128), seen_bytes(a), stream, a, n, src, dst);
+}
+
+cudaError_t launch_kv_compact(const KvArgs& a, cudaStream_t stream)
+{
+    cudaError_t e = launch_pdl(kv_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv_compact_move_kernel, dim3(148 * 8), dim3(kMoveThreads), 0, stream, a);
+}
+
+}  // namespace exl3

@@ -27,12 +27,17 @@ EXL3_ERR_ARCH = 5
 EXL3_ERR_CUDA = 6
 EXL3_ERR_TIMEOUT = 7
 EXL3_ERR_BOUNDS = 8
+EXL3_ERR_CACHE_FULL = 9
+EXL3_ERR_INDEX = 10
 
 # every entry point include/exl3.h declares
 EXPORTS = ("exl3_status_string", "exl3_last_cuda_error", "exl3_version", "exl3_workspace_bytes",
            "exl3_workspace_status", "exl3_kernel_launches", "exl3_decode_tiles", "exl3_hadamard128", "exl3_gemv",
            "exl3_gemm_small_m", "exl3_gemm_siblings", "exl3_large_m_workspace_bytes", "exl3_gemm_large_m",
-           "exl3_gemv_noalloc", "exl3_grouped_workspace_bytes", "exl3_gemm_grouped")
+           "exl3_gemv_noalloc", "exl3_grouped_workspace_bytes", "exl3_gemm_grouped", "exl3_q4_workspace_bytes",
+           "exl3_q4_gemm", "exl3_q4_pack", "exl3_kv_scratch_bytes", "exl3_kv_reset", "exl3_kv_status",
+           "exl3_kv_extend", "exl3_kv_write", "exl3_kv_truncate", "exl3_kv_fork", "exl3_kv_compact",
+           "exl3_paged_attention_workspace_bytes", "exl3_paged_attention")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libexl3.so not built ({LIB_PATH}); run `python -m gemm_exl3_gemv_b200.build`")
@@ -86,6 +91,39 @@ lib.exl3_grouped_workspace_bytes.argtypes = [_I, ctypes.POINTER(Problem), _I, _I
 lib.exl3_grouped_workspace_bytes.restype = _Z
 lib.exl3_gemm_grouped.argtypes = [_I, ctypes.POINTER(Problem), _I, _I, _I, _P, _Z, _P]
 lib.exl3_gemm_grouped.restype = _I
+
+_L, _F = ctypes.c_longlong, ctypes.c_float
+lib.exl3_q4_workspace_bytes.argtypes = [_I, _I, _I]
+lib.exl3_q4_workspace_bytes.restype = _Z
+lib.exl3_q4_gemm.argtypes = [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _Z, _P]
+lib.exl3_q4_gemm.restype = _I
+lib.exl3_q4_pack.argtypes = [_P, _I, _I, _P, _P]
+lib.exl3_q4_pack.restype = _I
+
+
+class Cache(ctypes.Structure):
+    """exl3_kv_cache_t: a paged key-value cache (device pointers and sizes)."""
+    _fields_ = [("k", _P), ("v", _P), ("table", _P), ("lens", _P), ("refs", _P), ("free", _P), ("scratch", _P),
+                ("n_layers", _I), ("n_pages", _I), ("n_heads", _I), ("page_size", _I), ("head_dim", _I),
+                ("n_seqs", _I), ("max_pages", _I)]
+
+
+# the cache argument is a pointer to a Cache (ctypes.byref)
+lib.exl3_kv_scratch_bytes.argtypes = [_I]
+lib.exl3_kv_scratch_bytes.restype = _Z
+lib.exl3_kv_reset.argtypes = [_P, _P]
+lib.exl3_kv_status.argtypes = [_P, _P]
+lib.exl3_kv_extend.argtypes = [_P, _I, _I, _P, _P, _P]
+lib.exl3_kv_write.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P, _L, _L, _P]
+lib.exl3_kv_truncate.argtypes = [_P, _I, _P, _P, _P]
+lib.exl3_kv_fork.argtypes = [_P, _I, _P, _P, _P]
+lib.exl3_kv_compact.argtypes = [_P, _P]
+lib.exl3_paged_attention_workspace_bytes.argtypes = [_I, _I, _I, _I]
+lib.exl3_paged_attention_workspace_bytes.restype = _Z
+lib.exl3_paged_attention.argtypes = [_P, _I, _I, _I, _P, _P, _P, _L, _L, _I, _F, _I, _I, _P, _L, _L, _P, _P, _Z, _P]
+for _name in ("reset", "status", "extend", "write", "truncate", "fork", "compact"):
+    getattr(lib, "exl3_kv_" + _name).restype = _I
+lib.exl3_paged_attention.restype = _I
 
 
 class Exl3Error(RuntimeError):
@@ -259,3 +297,92 @@ def gemm_grouped(problems, bits: int, fp32: bool = False, workspace: Optional[to
                                workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "exl3_gemm_grouped")
     return [p[5] for p in problems]
+
+
+# ------------------------------------------------- plain 4-bit weights ---
+
+def _expect(t: torch.Tensor, what: str, dtype, shape):
+    """A dense tensor of this type and shape on the current device, or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}")
+    _on_device(t, what)
+
+
+def _on_device(t: torch.Tensor, what: str):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device, got {t.device}")
+
+
+def _room(ws: torch.Tensor, need: int):
+    """Checks a workspace tensor and returns its bytes."""
+    _on_device(ws, "workspace")
+    if not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    n = ws.numel() * ws.element_size()
+    if n < need:
+        raise Exl3Error(EXL3_ERR_WORKSPACE, f"workspace of {n} bytes, {need} needed")
+    return n
+
+
+def q4_workspace_bytes(m: int, k_in: int, n_out: int) -> int:
+    return int(lib.exl3_q4_workspace_bytes(m, k_in, n_out))
+
+
+def q4_alloc_workspace(m: int, k_in: int, n_out: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace (uint8) for a 4-bit product of this size."""
+    n = q4_workspace_bytes(m, k_in, n_out)
+    if n == 0:
+        raise Exl3Error(EXL3_ERR_UNSUPPORTED, "q4_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def q4_pack(q: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """4-bit values (k_in, n_out) uint8 in the layout of ``q4_gemm``:
+    (n_out/16, k_in/64, 32, 4) int32.  Once per matrix, when it is loaded."""
+    if q.dim() != 2:
+        raise ValueError("q: expected (k_in, n_out)")
+    k_in, n_out = q.shape
+    _expect(q, "q", torch.uint8, (k_in, n_out))
+    if out is None:
+        out = torch.empty((n_out // 16, k_in // 64, 32, 4), dtype=torch.int32, device=q.device)
+    else:
+        _expect(out, "out", torch.int32, (n_out // 16, k_in // 64, 32, 4))
+    _check(lib.exl3_q4_pack(_ptr(q), k_in, n_out, _ptr(out), _stream(stream)), "exl3_q4_pack")
+    return out
+
+
+def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
+            group: int = 128, out: Optional[torch.Tensor] = None, fp32: bool = False,
+            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[i, n] = sum_k x[i, k] (q[k, n] - zero[k // group, n]) scale[k // group, n]
+    for x of shape (m, k_in), m <= 32, or (k_in,).  packed: from ``q4_pack``;
+    scale: (k_in / group, n_out) fp16; zero: the same in uint8 (0..15), None
+    for 8 everywhere.  Inference only: there is no backward pass."""
+    squeeze = x.dim() == 1
+    x2 = x.reshape(1, -1) if squeeze else x
+    if x2.dim() != 2 or packed.dim() != 4:
+        raise ValueError("expected x of (m, k_in) or (k_in,) and packed of (n_out/16, k_in/64, 32, 4)")
+    m, k_in = x2.shape
+    n_out = 16 * packed.shape[0]
+    if group not in (32, 64, 128) or k_in % group or k_in % 64 or not 1 <= m <= 32:
+        raise Exl3Error(EXL3_ERR_UNSUPPORTED, f"q4_gemm of {m} rows, k_in {k_in}, group {group}")
+    _expect(x2, "x", torch.float16, (m, k_in))
+    _expect(packed, "packed", torch.int32, (packed.shape[0], k_in // 64, 32, 4))
+    _expect(scale, "scale", torch.float16, (k_in // group, n_out))
+    if zero is not None:
+        _expect(zero, "zero", torch.uint8, (k_in // group, n_out))
+    if out is None:
+        out = torch.empty((m, n_out), dtype=torch.float32 if fp32 else torch.float16, device=x.device)
+    else:
+        if squeeze and out.dim() == 1:
+            out = out.view(1, -1)
+        _expect(out, "out", torch.float32 if fp32 else torch.float16, (m, n_out))
+    if workspace is None:
+        workspace = q4_alloc_workspace(m, k_in, n_out, device=x.device)
+    ws_bytes = _room(workspace, 0)
+    st = lib.exl3_q4_gemm(m, x2.data_ptr(), packed.data_ptr(), scale.data_ptr(),
+                          None if zero is None else zero.data_ptr(), out.data_ptr(), int(fp32), k_in, n_out, group,
+                          workspace.data_ptr(), ws_bytes, _stream(stream))
+    _check(st, "exl3_q4_gemm")
+    return out.reshape(-1) if squeeze else out

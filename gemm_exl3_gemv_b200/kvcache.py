@@ -1,0 +1,228 @@
+"""A paged key-value cache on the device, and the attention that reads it.
+
+Binding of the exl3_kv_* and exl3_paged_attention calls (include/exl3.h):
+argument checks and marshalling only.  The bookkeeping -- page tables, lengths,
+reference counts, free pages -- lives in device tensors and is read and written
+by the kernels alone, so every call can be captured in a CUDA graph and none
+waits for the host.  What the kernels find wrong (a bad list, too few pages) is
+therefore reported by ``KvCache.check()``, which synchronises.
+
+A step of a model with L layers, for a batch of sequences ``seqs``:
+
+    cache.extend(seqs, m)                               # room for m tokens each
+    for layer in range(L):
+        ...                                             # q, k, v products
+        cache.write(layer, seqs, k, v)
+        o = cache.attention(layer, seqs, q, workspace=ws)
+        ...                                             # o product, MLP
+    cache.truncate(seqs, accepted)                      # drop rejected tokens
+
+All calls work on the current CUDA device, which must be the cache's, and on
+the current stream or the one given.  Inference only: no backward pass.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import exl3 as ex
+
+MAX_LIST = 1024         # entries of a list of sequences
+MAX_ROWS = 32           # new tokens per sequence of one attention call
+
+
+class KvCache:
+    """k, v: (n_layers, n_pages, n_heads, page_size, head_dim) fp16; table:
+    (n_seqs, max_pages) int32; lens: (n_seqs,) int32; refs: (n_pages,) int32;
+    free: (ceil(n_pages / 32),) int32 bits.  The cache takes the tensors as
+    they are (``KvCache.empty`` makes and clears them)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                 refs: torch.Tensor, free: torch.Tensor):
+        if k.dim() != 5 or table.dim() != 2:
+            raise ValueError("expected k of (n_layers, n_pages, n_heads, page_size, head_dim) and table of "
+                             "(n_seqs, max_pages)")
+        n_layers, n_pages, n_heads, page_size, head_dim = k.shape
+        n_seqs, max_pages = table.shape
+        ex._expect(k, "k", torch.float16, k.shape)
+        ex._expect(v, "v", torch.float16, k.shape)
+        ex._expect(table, "table", torch.int32, (n_seqs, max_pages))
+        ex._expect(lens, "lens", torch.int32, (n_seqs,))
+        ex._expect(refs, "refs", torch.int32, (n_pages,))
+        ex._expect(free, "free", torch.int32, ((n_pages + 31) // 32,))
+        self.k, self.v, self.table, self.lens, self.refs, self.free = k, v, table, lens, refs, free
+        self.n_layers, self.n_pages, self.n_heads = n_layers, n_pages, n_heads
+        self.page_size, self.head_dim = page_size, head_dim
+        self.n_seqs, self.max_pages = n_seqs, max_pages
+        n = int(ex.lib.exl3_kv_scratch_bytes(n_pages))
+        if n == 0:
+            raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"a cache of {n_pages} pages")
+        self.scratch = torch.zeros(n, dtype=torch.uint8, device=k.device)
+        self.device = k.device
+        self._desc = ex.Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                              free.data_ptr(), self.scratch.data_ptr(), n_layers, n_pages, n_heads, page_size,
+                              head_dim, n_seqs, max_pages)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, n_layers: int, n_pages: int, n_heads: int, page_size: int, head_dim: int, n_seqs: int,
+              max_pages: int, device=None, stream=None) -> "KvCache":
+        """An empty cache with memory of its own (zero-filled keys and values)."""
+        device = device or "cuda"
+        pool = lambda: torch.zeros((n_layers, n_pages, n_heads, page_size, head_dim), dtype=torch.float16, device=device)
+        words = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
+        cache = cls(pool(), pool(), words(n_seqs, max_pages), words(n_seqs), words(n_pages), words((n_pages + 31) // 32))
+        cache.reset(stream)
+        return cache
+
+    # ------------------------------------------------------------ checks ---
+
+    def _list(self, t: torch.Tensor, what: str, n: Optional[int] = None) -> int:
+        if t.dim() != 1 or t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous one-dimensional int32 tensor")
+        if t.device != self.device:
+            raise ValueError(f"{what}: expected a tensor on {self.device}, got {t.device}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{what}: expected {n} entries, got {t.shape[0]}")
+        if t.shape[0] > MAX_LIST:
+            raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"{what}: a list of more than {MAX_LIST} entries")
+        return t.shape[0]
+
+    def _rows(self, t: torch.Tensor, what: str, n: int, heads: int):
+        """Checks (n, m, heads, head_dim) rows, dense within a row, and returns
+        m and the strides between entries and between rows."""
+        if t.dim() != 4 or t.dtype is not torch.float16 or t.shape[0] != n or t.shape[2] != heads or \
+                t.shape[3] != self.head_dim:
+            raise ValueError(f"{what}: expected fp16 of shape ({n}, m, {heads}, {self.head_dim}), got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{what}: expected a tensor on {self.device}, got {t.device}")
+        m, (s0, s1, s2, s3) = t.shape[1], t.stride()
+        if s3 != 1 or (s2 != self.head_dim and heads > 1) or (s1 % 8 and m > 1) or (s0 % 8 and n > 1):
+            raise ValueError(f"{what}: the heads of a row must lie one behind the other, rows and entries a multiple of "
+                             f"8 elements apart; strides are {t.stride()}")
+        return m, (s0 if n > 1 else 0), (s1 if m > 1 else 0)
+
+    def _here(self):
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+    # ------------------------------------------------------- bookkeeping ---
+
+    def reset(self, stream=None):
+        """No sequence holds anything, every page is free."""
+        self._here()
+        ex._check(ex.lib.exl3_kv_reset(self._ref, ex._stream(stream)), "exl3_kv_reset")
+
+    def status(self, stream=None) -> int:
+        """Synchronises, then reads and clears the fault word: EXL3_OK,
+        EXL3_ERR_CACHE_FULL or EXL3_ERR_INDEX.  While it is set, ``extend``
+        and ``write`` do nothing."""
+        self._here()
+        return int(ex.lib.exl3_kv_status(self._ref, ex._stream(stream)))
+
+    def check(self, stream=None):
+        """``status()`` as an exception."""
+        ex._check(self.status(stream), "KvCache")
+
+    def extend(self, seqs: torch.Tensor, m: int, counts: Optional[torch.Tensor] = None, stream=None):
+        """Each sequence of ``seqs`` grows by ``m`` tokens (counts: by
+        counts[b], 0..m), whose keys and values ``write`` then brings."""
+        n = self._list(seqs, "seqs")
+        if counts is not None:
+            self._list(counts, "counts", n)
+        self._here()
+        if n:
+            ex._check(ex.lib.exl3_kv_extend(self._ref, n, m, seqs.data_ptr(), None if counts is None else counts.data_ptr(),
+                                            ex._stream(stream)), "exl3_kv_extend")
+
+    def write(self, layer: int, seqs: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              counts: Optional[torch.Tensor] = None, stream=None):
+        """Keys and values (n, m, n_heads, head_dim) of the last m (counts:
+        counts[b]) tokens of each sequence, in one layer."""
+        n = self._list(seqs, "seqs")
+        if counts is not None:
+            self._list(counts, "counts", n)
+        m, bs, rs = self._rows(k, "k", n, self.n_heads)
+        if self._rows(v, "v", n, self.n_heads) != (m, bs, rs):
+            raise ValueError("k and v must have the same shape and strides")
+        self._here()
+        if n and m:
+            ex._check(ex.lib.exl3_kv_write(self._ref, layer, n, m, seqs.data_ptr(),
+                                           None if counts is None else counts.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                           bs, rs, ex._stream(stream)), "exl3_kv_write")
+
+    def truncate(self, seqs: torch.Tensor, lens: Optional[torch.Tensor] = None, stream=None):
+        """Each sequence keeps its first lens[b] tokens (None: it is freed)."""
+        n = self._list(seqs, "seqs")
+        if lens is not None:
+            self._list(lens, "lens", n)
+        self._here()
+        if n:
+            ex._check(ex.lib.exl3_kv_truncate(self._ref, n, seqs.data_ptr(), None if lens is None else lens.data_ptr(),
+                                              ex._stream(stream)), "exl3_kv_truncate")
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        """Each empty sequence dst[b] shares all of src[b] from now on."""
+        n = self._list(src, "src")
+        self._list(dst, "dst", n)
+        self._here()
+        if n:
+            ex._check(ex.lib.exl3_kv_fork(self._ref, n, src.data_ptr(), dst.data_ptr(), ex._stream(stream)), "exl3_kv_fork")
+
+    def compact(self, stream=None):
+        """Moves pages so that the used ones are the first of the pool."""
+        self._here()
+        ex._check(ex.lib.exl3_kv_compact(self._ref, ex._stream(stream)), "exl3_kv_compact")
+
+    # --------------------------------------------------------- attention ---
+
+    def attention_workspace(self, n: int, m: int, n_q_heads: int) -> torch.Tensor:
+        """Zero-filled workspace for attention calls with up to m rows per
+        sequence (any number n of sequences)."""
+        if n < 0:
+            raise ValueError("n: expected a number of sequences")
+        need = max(int(ex.lib.exl3_paged_attention_workspace_bytes(r, n_q_heads, self.n_heads, self.head_dim))
+                   for r in (m, 1))
+        if need == 0 or m < 1:
+            raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"attention of {m} rows with {n_q_heads} heads")
+        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+
+    def attention(self, layer: int, seqs: torch.Tensor, q: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of the last m (counts: counts[b]) tokens of each sequence,
+        q: (n, m, n_q_heads, head_dim), over that sequence.  Row i sees the
+        tokens up to its own; with ``window`` only the last ``window`` of them
+        and the first ``sinks`` of the sequence.  scale: 1/sqrt(head_dim) by
+        default.  lse: (n, m, n_q_heads) fp32, filled with the logarithms of
+        the softmax sums.  Rows from counts[b] on are left as they were (in an
+        ``out`` made here: zero)."""
+        n = self._list(seqs, "seqs")
+        if counts is not None:
+            self._list(counts, "counts", n)
+        heads = q.shape[2] if q.dim() == 4 else 0
+        m, qb, qr = self._rows(q, "q", n, heads)
+        if out is None:
+            make = torch.empty if counts is None else torch.zeros
+            out = make((n, m, heads, self.head_dim), dtype=torch.float16, device=self.device)
+        mo, ob, orow = self._rows(out, "out", n, heads)
+        if mo != m:
+            raise ValueError(f"out: expected {m} rows per sequence, got {mo}")
+        if lse is not None:
+            ex._expect(lse, "lse", torch.float32, (n, m, heads))
+        self._here()
+        if n == 0 or m == 0:
+            return out
+        if workspace is None:
+            workspace = self.attention_workspace(n, m, heads)
+        ws_bytes = ex._room(workspace, 0)
+        ex._check(ex.lib.exl3_paged_attention(
+            self._ref, layer, n, m, seqs.data_ptr(), None if counts is None else counts.data_ptr(), q.data_ptr(), qb, qr,
+            heads, 1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, sinks, out.data_ptr(), ob, orow,
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(), ws_bytes, ex._stream(stream)),
+            "exl3_paged_attention")
+        return out

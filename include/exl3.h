@@ -69,8 +69,12 @@ enum {
     EXL3_ERR_CUDA = 6,         /* a CUDA runtime call failed                     */
     EXL3_ERR_TIMEOUT = 7,      /* a kernel's bounded wait expired (see
                                   exl3_workspace_status)                         */
-    EXL3_ERR_BOUNDS = 8        /* debug builds only: an index check inside a
+    EXL3_ERR_BOUNDS = 8,       /* debug builds only: an index check inside a
                                   kernel failed (see exl3_workspace_status)      */
+    EXL3_ERR_CACHE_FULL = 9,   /* a cache ran out of pages, or a sequence out of
+                                  table entries (see exl3_kv_status)             */
+    EXL3_ERR_INDEX = 10        /* a list given to a cache call, or the cache's own
+                                  bookkeeping, held a bad index (exl3_kv_status) */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -300,6 +304,186 @@ EXL3_API int exl3_gemm_grouped(int m, const exl3_problem_t *probs, int n_probs, 
 EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
                                const uint16_t *su, const uint16_t *sv, void *y, int y_fp32,
                                int k_in, int n_out, int bits, void *stream);
+
+/*
+ * exl3_q4_gemm -- products with plain 4-bit weights in groups:
+ *     y[i][n] = sum_k x[i][k] * (q[k][n] - zero[k/group][n]) * scale[k/group][n]
+ * the form in which models keep the matrices that are not trellis-coded.
+ *   m      : 1 .. 32 rows (decode, verification).   x : m x k_in fp16, row-major.
+ *   packed : the 4-bit values in the layout below, k_in*n_out/2 bytes.
+ *   scale  : (k_in/group) x n_out fp16, row-major.
+ *   zero   : (k_in/group) x n_out uint8, each 0..15; NULL means 8 everywhere.
+ *            Larger values are taken as they are (no fault).
+ *   y      : m x n_out, fp16 (y_fp32 == 0) or fp32, row-major.
+ *   group  : 32, 64 or 128.   k_in : positive multiple of 64 and of group, at
+ *            most 2^20.   n_out : positive multiple of 16, at most 1,048,576.
+ *   workspace, ws_bytes : at least exl3_q4_workspace_bytes(m, k_in, n_out)
+ *            bytes, 256-byte aligned, zero-filled before first use; shared by
+ *            calls on one stream as described at exl3_workspace_bytes (it may
+ *            be the same buffer as the trellis products').
+ * Layout of packed: tiles of 16 channels x 64 inputs, tile (tn, tk) at
+ *   (tn*(k_in/64) + tk)*128 uint32 words; word 4*(4*g + t) + j of a tile
+ *   (g < 8, t < 4, j < 4) holds channels 16*tn + g + 8*c, c < 2, and inputs
+ *   64*tk + 32*(j/2) + 8*t + 4*(j%2) + i, i < 4, each value at bit
+ *   4*c + 8*(i/2) + 16*(i%2).
+ * The weights enter the tensor cores as exact integers q - zero, products are
+ * summed in fp32, and each group's sum is scaled in fp32.  The order of every
+ * sum is fixed: repeated calls are bitwise identical.
+ */
+EXL3_API size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out);
+EXL3_API int exl3_q4_gemm(int m, const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
+                          const uint8_t *zero, void *y, int y_fp32, int k_in, int n_out, int group,
+                          void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * exl3_q4_pack -- lay 4-bit values out for exl3_q4_gemm.
+ *   q : k_in x n_out uint8, row-major (the low four bits of each are taken).
+ *   packed : k_in*n_out/2 bytes out.   k_in a multiple of 64, n_out of 16.
+ */
+EXL3_API int exl3_q4_pack(const uint8_t *q, int k_in, int n_out, uint32_t *packed, void *stream);
+
+/*
+ * A paged key-value cache: what the attention between the q, k, v and o
+ * products of a layer reads.  The rdna4-recipe page names attention for
+ * grouped heads over the cache beside its verify products (section "What we
+ * added on top of upstream"); the layout here is this library's own.
+ *
+ *   k, v   : n_layers x n_pages x n_heads x page_size x head_dim fp16.  Token t
+ *            of a sequence lies in its page number t / page_size, at row
+ *            t % page_size of each head.  A page id stands for that page of
+ *            every layer.
+ *   table  : n_seqs x max_pages int32: the page ids of each sequence, in
+ *            order; -1 behind the last.
+ *   lens   : n_seqs int32: tokens of each sequence (0: it holds nothing).
+ *   refs   : n_pages int32: how many sequences hold each page.
+ *   free   : ceil(n_pages / 32) uint32: bit p % 32 of word p / 32 is set while
+ *            page p is free; bits past n_pages are zero.
+ *   scratch: exl3_kv_scratch_bytes(n_pages) bytes, zero-filled before first use.
+ * All arrays are device memory of the caller.  exl3_kv_reset() makes an empty
+ * cache of them.  The bookkeeping is read and written on the device only, so
+ * every call can be captured in a CUDA graph and no call waits for the host.
+ *   head_dim : 64 or 128.   page_size : 16, 32, 64, 128 or 256.
+ *   n_heads  : 1 .. 256.    n_pages : 1 .. 2^20.   n_seqs : 1 .. 65536.
+ *   max_pages: 1 .. 2^20, max_pages * page_size <= 2^30.   n_layers : 1 .. 1024.
+ *   n_pages * n_heads * page_size < 2^31.
+ * Calls on one cache must be ordered (one stream, or events).
+ *
+ * Lists: `seqs` (and src, dst) are n int32 sequence numbers in device memory,
+ * n <= 1024, each sequence at most once in a call (lists, counts and new
+ * lengths need only 4-byte alignment).  They are checked on the
+ * device: a number out of range or a repeated one makes the whole call do
+ * nothing and is reported by exl3_kv_status as EXL3_ERR_INDEX.
+ */
+typedef struct exl3_kv_cache {
+    uint16_t *k;
+    uint16_t *v;
+    int32_t *table;
+    int32_t *lens;
+    int32_t *refs;
+    uint32_t *free;
+    void *scratch;
+    int n_layers;
+    int n_pages;
+    int n_heads;
+    int page_size;
+    int head_dim;
+    int n_seqs;
+    int max_pages;
+} exl3_kv_cache_t;
+
+EXL3_API size_t exl3_kv_scratch_bytes(int n_pages);
+
+/* exl3_kv_reset -- no sequence holds anything, every page is free. */
+EXL3_API int exl3_kv_reset(const exl3_kv_cache_t *cache, void *stream);
+
+/*
+ * exl3_kv_status -- synchronises `stream`, reads and clears the cache's fault
+ * word: EXL3_OK, EXL3_ERR_CACHE_FULL or EXL3_ERR_INDEX (where both, INDEX).
+ * While it is set, exl3_kv_extend and exl3_kv_write do nothing, so a step
+ * whose extend was refused leaves the cache as it was.
+ */
+EXL3_API int exl3_kv_status(const exl3_kv_cache_t *cache, void *stream);
+
+/*
+ * exl3_kv_extend -- sequence seqs[b] grows by counts[b] tokens (0..m; counts
+ * NULL: by m), b < n.  New pages are the lowest free ones, given out in the
+ * order of the list; a partly filled last page that other sequences hold too
+ * is first replaced by a copy of its tokens in every layer.  If the free
+ * pages or a sequence's table entries do not suffice, nothing changes and
+ * exl3_kv_status reports EXL3_ERR_CACHE_FULL.  Once per step, for all layers.
+ */
+EXL3_API int exl3_kv_extend(const exl3_kv_cache_t *cache, int n, int m, const int32_t *seqs,
+                            const int32_t *counts, void *stream);
+
+/*
+ * exl3_kv_write -- layer `layer` gets the keys and values of the last
+ * counts[b] tokens of seqs[b], after the exl3_kv_extend with the same list.
+ *   k_new, v_new : row i of entry b at element b*batch_stride + i*row_stride,
+ *                  n_heads x head_dim fp16 each; strides multiples of 8.
+ * Rows i >= counts[b] are not read.
+ */
+EXL3_API int exl3_kv_write(const exl3_kv_cache_t *cache, int layer, int n, int m, const int32_t *seqs,
+                           const int32_t *counts, const uint16_t *k_new, const uint16_t *v_new,
+                           long long batch_stride, long long row_stride, void *stream);
+
+/*
+ * exl3_kv_truncate -- sequence seqs[i] keeps its first new_lens[i] tokens (all
+ * of them if it has fewer; new_lens NULL: none, it is freed).  A page that no
+ * sequence holds any more is free.
+ */
+EXL3_API int exl3_kv_truncate(const exl3_kv_cache_t *cache, int n, const int32_t *seqs, const int32_t *new_lens,
+                              void *stream);
+
+/*
+ * exl3_kv_fork -- sequence dst[i], which holds nothing, shares all pages of
+ * src[i] from now on; no key or value is copied (exl3_kv_extend copies a
+ * shared last page when one of its holders grows).  A source may appear
+ * several times; a sequence that is both a source and a destination is
+ * refused (EXL3_ERR_INDEX), and a pair whose destination holds tokens is
+ * left out (EXL3_ERR_INDEX).
+ */
+EXL3_API int exl3_kv_fork(const exl3_kv_cache_t *cache, int n, const int32_t *src, const int32_t *dst, void *stream);
+
+/*
+ * exl3_kv_compact -- moves pages so that the n used ones are pages 0..n-1: the
+ * i-th used page behind the border goes to the i-th free one before it
+ * (both ascending), in every layer, and the tables follow.
+ */
+EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
+
+/*
+ * exl3_paged_attention -- attention of the last counts[b] tokens of sequence
+ * seqs[b] (counts NULL: m) over that sequence in layer `layer`:
+ *   row i sits at position p = lens - counts + i and sees the tokens t <= p
+ *   with t > p - window or t < sinks (window 0: all t <= p);
+ *   out[i][h] = sum_t w_t v_t,  w = softmax(scale * q[i][h] . k_t), where query
+ *   head h reads head h / (n_q_heads / n_heads) of the cache.
+ *   m    : 1 .. 32 rows per sequence (1: decode; more: drafted tokens).
+ *   q    : row i of entry b at element b*q_batch_stride + i*q_row_stride,
+ *          n_q_heads x head_dim fp16.   n_q_heads : a multiple of n_heads, at
+ *          most 32 of them per head of the cache.
+ *   out  : as q, with its own strides.   lse : n x m x n_q_heads fp32, the
+ *          natural logarithm of each softmax's sum of exponentials; or NULL.
+ *   scale: finite.   window, sinks : >= 0.
+ *   workspace, ws_bytes : at least exl3_paged_attention_workspace_bytes(...)
+ *          bytes, 256-byte aligned, zero-filled before first use, shared by
+ *          calls on one stream.
+ * Rows i >= counts[b] of out and lse are left as they were.  A row that sees
+ * no token gets zeros (lse -inf).  Keys and values that a row does not see
+ * have no influence on it, whatever they hold.  Scores, the softmax's
+ * statistics and the weighted sums are fp32.  The order of every sum depends
+ * on the lengths alone: repeated calls are bitwise identical.
+ * A table entry out of range is not followed: exl3_kv_status then reports
+ * EXL3_ERR_INDEX, and the rows that needed it are not valid; the same for a
+ * bad number in seqs, whose rows are left as they were.  Bounded waits as in
+ * exl3_gemm_small_m (exl3_workspace_status).
+ */
+EXL3_API size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
+EXL3_API int exl3_paged_attention(const exl3_kv_cache_t *cache, int layer, int n, int m, const int32_t *seqs,
+                                  const int32_t *counts, const uint16_t *q, long long q_batch_stride,
+                                  long long q_row_stride, int n_q_heads, float scale, int window, int sinks,
+                                  uint16_t *out, long long out_batch_stride, long long out_row_stride, float *lse,
+                                  void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
