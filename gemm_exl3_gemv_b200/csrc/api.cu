@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" entry points of libexl3 (declared in include/exl3.h):
 // argument validation on the host, architecture check, dispatch to kernels.
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -22,19 +23,24 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool bits_ok(int bits) { return bits == 2 || bits == 3 || bits == 4; }
 
-// The kernels are built for sm_100a only; check the current device once per
-// call (cheap: cached attribute queries in the runtime).
+// The kernels are built for sm_100a only; the current device is looked up at
+// each call, its architecture once.
 int check_arch()
 {
+    static std::atomic<signed char> known[64];            // per device: 0 not asked yet, 1 sm_100, -1 another
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
+    if (dev >= 0 && dev < 64)
+        if (const signed char k = known[dev].load(std::memory_order_relaxed)) return k > 0 ? EXL3_OK : EXL3_ERR_ARCH;
     int major = 0, minor = 0;
     e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (e != cudaSuccess) return cuda_fail(e);
     e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    return (major == 10 && minor == 0) ? EXL3_OK : EXL3_ERR_ARCH;
+    const bool ok = major == 10 && minor == 0;
+    if (dev >= 0 && dev < 64) known[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
+    return ok ? EXL3_OK : EXL3_ERR_ARCH;
 }
 
 int validate_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale, const uint16_t* su,

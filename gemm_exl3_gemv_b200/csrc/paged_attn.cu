@@ -39,6 +39,11 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // Probabilities carry a factor 2^kUp on their way through fp16 (it cancels in
 // o): the largest is 2^14, and what is 2^-28 of it is still a normal number.
 constexpr float kUp = 14.f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Tiles per CTA from which another CTA is worth its part of the join.
+constexpr int kMinTiles = 4;
+constexpr int kFan = 8;                                      // parts joined at once
+constexpr int kMaxCtas = 148 * 2;
 
 struct AttnPlan {
     int row_tiles;            // row tiles of a (sequence, head)
@@ -49,8 +54,7 @@ struct AttnPlan {
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -74,6 +78,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 0xffff for each half of the pair that is finite (x * 0 is NaN for the others)
+__device__ __forceinline__ uint32_t finite_halves(uint32_t u)
+{
+    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(0.f));
+    return __heq2_mask(z, z);
 }
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
 {
@@ -129,10 +139,132 @@ struct AttnShape {
     static constexpr int kRows = 16 * WR;
     static constexpr int kHalf = kTile * D * 2;              // bytes of a tile's keys (or values)
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kJoin = WT > 1 ? (WT / 2) * kRows * (D + 2) * 4 : 0;
+    // shared memory for joining the warps, and the statistics of joined parts
+    static constexpr int kJoin = WT > 1 ? (WT / 2) * kRows * (D + 2) * 4 : (kConsumers + kRows) * 8;
     static constexpr int kSmem = kStages * 2 * kHalf + kJoin + 256;   // two CTAs per SM fit
-    static constexpr int kSlot = kRows * (D + 2);            // floats of a partial result
+    static constexpr int kSlotRow = D + 4;                   // a row of a partial result: D sums, maximum, sum
+    static constexpr int kSlot = kRows * kSlotRow;
 };
+
+// Counts the calling CTA in; true in the last of `of` CTAs, which may then read
+// what the others wrote before they were counted.  Consumer threads.
+__device__ __forceinline__ bool last_of(uint32_t* counter, int of, int& flag, int tid, int threads)
+{
+    __threadfence();
+    named_bar(1, threads);
+    if (tid == 0) {
+        flag = atomicAdd(counter, 1u) == (uint32_t)of - 1;
+        if (flag) *counter = 0;
+    }
+    named_bar(1, threads);
+    const bool last = flag;
+    if (last) __threadfence();
+    return last;
+}
+
+// Parts of a group, joined by the consumers of one CTA in the order of the
+// parts: written out (LAST), or to the first part's slot.  First every row's
+// maximum and sum, several threads a row; then the weighted sums, a float4 of
+// kAcc rows a thread, kDeep parts in flight (the parts lie in the L2; their
+// latency is the cost).
+template <typename S, int D, bool LAST, typename SlotOf>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, int b, int h, float* slots, int parts,
+                                           SlotOf slot_of, float* smem, int tid)
+{
+    constexpr int kSides = S::kConsumers / S::kRows;
+    float2* side = reinterpret_cast<float2*>(smem);
+    float2* row_stat = side + S::kConsumers;                 // maximum, 1 / sum
+    auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
+    {
+        const int r = tid % S::kRows, first = tid / S::kRows;
+        float m = kNegInf, l = 0.f;
+#pragma unroll 4
+        for (int c = first; c < parts; c += kSides) {
+            const float2 ms = __ldcg(reinterpret_cast<const float2*>(part_of(c) + r * S::kSlotRow + D));
+            const float now = fmaxf(m, ms.x), c0 = now == kNegInf ? 0.f : now;
+            l = l * ex2(m - c0) + ms.y * ex2(ms.x - c0);
+            m = now;
+        }
+        side[tid] = make_float2(m, l);
+    }
+    named_bar(1, S::kConsumers);
+    if (tid < S::kRows) {
+        float m = kNegInf, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSides; ++i) {
+            const float2 ms = side[i * S::kRows + tid];
+            const float now = fmaxf(m, ms.x), c0 = now == kNegInf ? 0.f : now;
+            l = l * ex2(m - c0) + ms.y * ex2(ms.x - c0);
+            m = now;
+        }
+        row_stat[tid] = make_float2(m == kNegInf ? 0.f : m, 1.f);
+        if constexpr (LAST) {
+            const int rr = en.row0 + tid, tok = rr / a.group;
+            const bool none = en.len - en.count + tok < 0;   // a row that sees no token: zeros
+            row_stat[tid].y = none ? 0.f : 1.f / l;
+            if (a.lse && tid < en.rows)
+                a.lse[((long long)b * a.m + tok) * a.n_q_heads + h * a.group + rr % a.group] =
+                    none ? kNegInf : (m + (log2f(l) - kUp)) * kLn2;
+        } else {
+            side[tid] = make_float2(m, l);                   // this thread alone reads and writes it from here on
+        }
+    }
+    named_bar(1, S::kConsumers);
+    constexpr int kVec = D / 4, kStep = S::kConsumers / kVec;    // rows apart
+    constexpr int kAcc = S::kRows / kStep < 4 ? S::kRows / kStep : 4, kDeep = 4;
+    const int col = 4 * (tid % kVec);
+    for (int r0 = tid / kVec; r0 < S::kRows; r0 += kStep * kAcc) {
+        float4 acc[kAcc];
+        float top[kAcc];
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) {
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            top[i] = row_stat[r0 + i * kStep].x;
+        }
+        for (int c0 = 0; c0 < parts; c0 += kDeep) {
+            float4 v[kDeep][kAcc];
+            float w[kDeep][kAcc];
+#pragma unroll
+            for (int c = 0; c < kDeep; ++c) {
+                const float* from = part_of(min(c0 + c, parts - 1));
+#pragma unroll
+                for (int i = 0; i < kAcc; ++i) {
+                    const float* at = from + (r0 + i * kStep) * S::kSlotRow;
+                    v[c][i] = __ldcg(reinterpret_cast<const float4*>(at + col));
+                    w[c][i] = __ldcg(at + D);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kDeep; ++c) {
+                if (c0 + c >= parts) break;
+#pragma unroll
+                for (int i = 0; i < kAcc; ++i) {
+                    const float f = ex2(w[c][i] - top[i]);
+                    acc[i].x += f * v[c][i].x;
+                    acc[i].y += f * v[c][i].y;
+                    acc[i].z += f * v[c][i].z;
+                    acc[i].w += f * v[c][i].w;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) {
+            const int r = r0 + i * kStep;
+            if constexpr (LAST) {
+                if (r >= en.rows) break;
+                const int rr = en.row0 + r, tok = rr / a.group;
+                const float inv = row_stat[r].y;
+                *reinterpret_cast<uint2*>(a.out + b * a.o_bs + tok * a.o_rs + (long long)(h * a.group + rr % a.group) * D + col) =
+                    make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
+            } else {
+                __stcg(reinterpret_cast<float4*>(part_of(0) + r * S::kSlotRow + col), acc[i]);
+            }
+        }
+    }
+    named_bar(1, S::kConsumers);
+    if constexpr (!LAST)                                     // after every thread has read the first part's maxima
+        if (tid < S::kRows) __stcg(reinterpret_cast<float2*>(part_of(0) + tid * S::kSlotRow + D), side[tid]);
+}
 
 template <int D, int WR, int WT>
 __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
@@ -156,6 +288,8 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     uint32_t* status = reinterpret_cast<uint32_t*>(a.ws);
     if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, WR * WT);
@@ -186,7 +320,7 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
         total += scan[w];
     }
     if (total == 0) return;
-    const long long ctas = min((long long)gridDim.x, total), cta = blockIdx.x;
+    const long long ctas = min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles), cta = blockIdx.x;
     if (cta >= ctas) return;
     const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
     if (u0 >= before && u0 < before + mine) {
@@ -307,6 +441,9 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
         const int p_last = en.len - en.count + (en.row0 + en.rows - 1) / a.group;
         const int all_hi = p_first + 1, all_lo = a.window ? p_last - a.window + 1 : 0;
 
+        auto sees = [&](int p, int tk) { return tk <= p && (!a.window || tk > p - a.window || tk < a.sinks); };
+        auto any_sees = [&](int tk) { return tk <= p_last && (!a.window || tk > p_first - a.window || tk < a.sinks); };
+
         for (int it = 0; it < n; ++it) {
             const int tok0 = tile_at(en, off + it) * kTile;
             if (alive) {
@@ -323,11 +460,11 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NS; j += 2) {
-                const int row = wt * TPW + j * 8 + lm_row;
+            for (int k = 0; k < D / 16; ++k) {
+                const int chunk = 2 * k + lm_col;            // 16-byte piece of the row
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int chunk = 2 * k + lm_col;        // 16-byte piece of the row
+                for (int j = 0; j < NS; j += 2) {
+                    const int row = wt * TPW + j * 8 + lm_row;
                     uint32_t f[4];
                     ldsm4(f, kt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
                     mma_16816(s[j], qf[k], f[0], f[2]);
@@ -341,8 +478,7 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tk = tok0 + wt * TPW + j * 8 + 2 * t + (i & 1), p = pos[i >> 1];
-                        const bool see = tk <= p && (!a.window || tk > p - a.window || tk < a.sinks);
-                        s[j][i] = see ? s[j][i] * pl.scale_log2 : kNegInf;
+                        s[j][i] = sees(p, tk) ? s[j][i] * pl.scale_log2 : kNegInf;
                     }
             } else {
 #pragma unroll
@@ -381,72 +517,77 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
                     sum[i >> 1] += s[j][i];
                 }
             // values
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < NS; j += 2) {
-                const uint32_t pa[4] = {pack2(s[j][0], s[j][1]), pack2(s[j][2], s[j][3]), pack2(s[j + 1][0], s[j + 1][1]),
-                                        pack2(s[j + 1][2], s[j + 1][3])};
-                const int row = wt * TPW + j * 8 + lm_row;
-                // tokens 2t, 2t+1 (lo) and 2t+8, 2t+9 (hi) of the k-step, which this lane's value fragments hold
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (!whole) {
+                for (int j = 0; j < NS; j += 2) {
+                    const uint32_t pa[4] = {pack2(s[j][0], s[j][1]), pack2(s[j][2], s[j][3]), pack2(s[j + 1][0], s[j + 1][1]),
+                                            pack2(s[j + 1][2], s[j + 1][3])};
+                    const int row = wt * TPW + j * 8 + lm_row;
+#pragma unroll
+                    for (int d = 0; d < ND; d += 2) {
+                        const int chunk = d + lm_col;
+                        uint32_t f[4];
+                        ldsm4t(f, vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+                        mma_16816(o[d], pa, f[0], f[1]);
+                        mma_16816(o[d + 1], pa, f[2], f[3]);
+                    }
+                }
+            } else {
+                uint32_t finite = 0xffffffffu;
+#pragma unroll
+                for (int j = 0; j < NS; j += 2) {
+                    const uint32_t pa[4] = {pack2(s[j][0], s[j][1]), pack2(s[j][2], s[j][3]), pack2(s[j + 1][0], s[j + 1][1]),
+                                            pack2(s[j + 1][2], s[j + 1][3])};
+                    const int row = wt * TPW + j * 8 + lm_row;
+                    // tokens 2t, 2t+1 (0) and 2t+8, 2t+9 (1) of the k-step, which this lane's fragments hold: does any
+                    // row of the tile see them?
+                    uint32_t keep[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int tk = tok0 + wt * TPW + j * 8 + 2 * t + 8 * i;
-                        keep[i] = (tk <= p_last ? 0xffffu : 0u) | (tk + 1 <= p_last ? 0xffff0000u : 0u);
-                        if (a.window) {
-                            const int first = p_first - a.window;    // the tile's first row sees tokens behind this one
-                            if (tk <= first && tk >= a.sinks) keep[i] &= 0xffff0000u;
-                            if (tk + 1 <= first && tk + 1 >= a.sinks) keep[i] &= 0xffffu;
+                        keep[i] = (any_sees(tk) ? 0xffffu : 0u) | (any_sees(tk + 1) ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int d = 0; d < ND; d += 2) {
+                        const int chunk = d + lm_col;
+                        uint32_t f[4];
+                        ldsm4t(f, vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[i] &= keep[i & 1];
+                            const uint32_t ok = finite_halves(f[i]);
+                            finite &= ok;
+                            f[i] &= ok;
                         }
+                        mma_16816(o[d], pa, f[0], f[1]);
+                        mma_16816(o[d + 1], pa, f[2], f[3]);
                     }
                 }
+                if (__any_sync(0xffffffffu, finite != 0xffffffffu)) {
+                    // values that are not finite were left out: only the rows that see them get them
+                    for (int x = 0; x < TPW; ++x) {
+                        const int tk = tok0 + wt * TPW + x, row = wt * TPW + x;
+                        float p[2];
 #pragma unroll
-                for (int d = 0; d < ND; d += 2) {
-                    const int chunk = d + lm_col;
-                    uint32_t f[4];
-                    ldsm4t(f, vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-                    if (!whole) {
-                        f[0] &= keep[0];
-                        f[1] &= keep[1];
-                        f[2] &= keep[0];
-                        f[3] &= keep[1];
-                        bool odd = false;
+                        for (int i = 0; i < 2; ++i) {
+                            float mine = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            odd |= (f[i] & 0x7c00u) == 0x7c00u || (f[i] & 0x7c000000u) == 0x7c000000u;
-                        if (__any_sync(0xffffffffu, odd)) {
-                            // a value that is not finite and that some rows may not see: row by row
-                            for (int r = 0; r < 16; ++r) {
-                                const int rr = wr * 16 + r;
-                                if (rr >= en.rows) break;
-                                const int p = en.len - en.count + (en.row0 + rr) / a.group;
-                                uint32_t see[2];
+                            for (int j = 0; j < NS; ++j)
+                                if (x >> 3 == j) mine = x & 1 ? s[j][2 * i + 1] : s[j][2 * i];
+                            p[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) | ((x & 7) >> 1));
+                        }
+                        if (!any_sees(tk)) continue;
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const int tk = tok0 + wt * TPW + j * 8 + 2 * t + 8 * i;
-                                    see[i] = 0;
-#pragma unroll
-                                    for (int x = 0; x < 2; ++x)
-                                        if (tk + x <= p && (!a.window || tk + x > p - a.window || tk + x < a.sinks))
-                                            see[i] |= 0xffffu << (16 * x);
-                                }
-                                float one[2][4] = {};
-                                mma_16816(one[0], pa, f[0] & see[0], f[1] & see[1]);
-                                mma_16816(one[1], pa, f[2] & see[0], f[3] & see[1]);
-                                if (g == (r & 7)) {
-                                    const int i = r >> 3;
-#pragma unroll
-                                    for (int x = 0; x < 2; ++x) {
-                                        o[d][2 * i + x] += one[0][2 * i + x];
-                                        o[d + 1][2 * i + x] += one[1][2 * i + x];
-                                    }
-                                }
-                            }
-                            continue;
+                        for (int d = 0; d < ND; ++d) {
+                            uint32_t v;
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
+                                         : "r"(vt + (d >> 3) * (kTile * 128) + row * 128 + (((d & 7) ^ (row & 7)) << 4) + 4 * t));
+                            v &= ~finite_halves(v);
+                            const float2 vv = __half22float2(*reinterpret_cast<const __half2*>(&v));
+                            if (sees(pos[0], tk)) { o[d][0] += p[0] * vv.x; o[d][1] += p[0] * vv.y; }
+                            if (sees(pos[1], tk)) { o[d][2] += p[1] * vv.x; o[d][3] += p[1] * vv.y; }
                         }
                     }
-                    mma_16816(o[d], pa, f[0], f[1]);
-                    mma_16816(o[d + 1], pa, f[2], f[3]);
                 }
             }
             __syncwarp();
@@ -495,77 +636,58 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
             named_bar(1, S::kConsumers);
         }
 
-        const bool complete = n == en.tiles;
         const long long gstart = base + (long long)h * en.tiles;
-        bool finish = complete;
-        if (!complete) {
+        if (n == en.tiles) {
+            if (wt == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = wr * 16 + g + 8 * i;
+                    if (r >= en.rows) continue;
+                    const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr % a.group;
+                    const float inv = pos[i] < 0 ? 0.f : 1.f / sum[i];    // a row that sees no token: zeros
+                    uint16_t* out = a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+                        *reinterpret_cast<uint32_t*>(out + 8 * d + 2 * t) = pack2(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
+                    if (a.lse && t == 0)
+                        a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] =
+                            pos[i] < 0 ? kNegInf : (mx[i] + (log2f(sum[i]) - kUp)) * kLn2;
+                }
+            }
+        } else {
             // ---- partial result to this CTA's slot; the last CTA of the group joins ----
             float* slots = reinterpret_cast<float*>(a.ws + ws_data_off());
             float* slot = slots + (2 * cta + (first_segment ? 0 : 1)) * S::kSlot;
             if (wt == 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float* at = slot + (wr * 16 + g + 8 * i) * (D + 2);
+                    float* at = slot + (wr * 16 + g + 8 * i) * S::kSlotRow;
 #pragma unroll
                     for (int d = 0; d < ND; ++d)
                         __stcg(reinterpret_cast<float2*>(at + 8 * d + 2 * t), make_float2(o[d][2 * i], o[d][2 * i + 1]));
                     if (t == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
                 }
             }
-            __threadfence();
-            named_bar(1, S::kConsumers);
+            // the group's parts: the first one is its CTA's first or last segment, the others first segments
             const int c_first = cta_of_unit(gstart, ctas, total), c_last = cta_of_unit(gstart + en.tiles - 1, ctas, total);
-            uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off()) + c_first;
-            if (tid == 0) last_flag = atomicAdd(counter, 1u) == (uint32_t)(c_last - c_first);
-            named_bar(1, S::kConsumers);
-            finish = last_flag;
-            if (finish) {
-                if (tid == 0) *counter = 0;
-                __threadfence();
-                if (wt == 0) {
-                    const bool front = gstart == total * c_first / ctas;   // the group opens its first CTA's range
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) { mx[i] = kNegInf; sum[i] = 0.f; }
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float* from = slots + (2LL * c + (c == c_first && !front ? 1 : 0)) * S::kSlot;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float* at = from + (wr * 16 + g + 8 * i) * (D + 2);
-                            const float2 ms = __ldcg(reinterpret_cast<const float2*>(at + D));
-                            const float now = fmaxf(mx[i], ms.x), c0 = now == kNegInf ? 0.f : now;
-                            const float f1 = ex2(mx[i] - c0), f2 = ex2(ms.x - c0);
-                            mx[i] = now;
-                            sum[i] = sum[i] * f1 + ms.y * f2;
-#pragma unroll
-                            for (int d = 0; d < ND; ++d) {
-                                const float2 v = __ldcg(reinterpret_cast<const float2*>(at + 8 * d + 2 * t));
-                                o[d][2 * i] = o[d][2 * i] * f1 + v.x * f2;
-                                o[d][2 * i + 1] = o[d][2 * i + 1] * f1 + v.y * f2;
-                            }
-                        }
-                    }
+            const int parts = c_last - c_first + 1, late = gstart == total * c_first / ctas ? 0 : 1;
+            auto slot_of = [&](int c) { return 2 * (c_first + c) + (c == 0 ? late : 0); };
+            const int mine = (int)cta - c_first;
+            // up to kFan parts are joined at once, more in two levels of about the square root
+            int fan = parts;
+            if (parts > kFan)
+                for (fan = kFan / 2; fan * fan < parts; ++fan) {}
+            uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off());
+            const int node = mine / fan * fan, in_node = min(fan, parts - node);
+            if (last_of(counters + slot_of(node), in_node, last_flag, tid, S::kConsumers)) {
+                if (fan == parts) {
+                    join_parts<S, D, true>(a, en, b, h, slots, parts, slot_of, join, tid);
+                } else {
+                    join_parts<S, D, false>(a, en, b, h, slots, in_node, [&](int c) { return slot_of(node + c); }, join, tid);
+                    const int nodes = (parts + fan - 1) / fan;
+                    if (last_of(counters + 2 * kMaxCtas + slot_of(0), nodes, last_flag, tid, S::kConsumers))
+                        join_parts<S, D, true>(a, en, b, h, slots, nodes, [&](int c) { return slot_of(c * fan); }, join, tid);
                 }
-            }
-        }
-        if (finish && wt == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = wr * 16 + g + 8 * i;
-                if (r >= en.rows) continue;
-                const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr % a.group;
-                // a row that sees no token: zeros
-                const float inv = pos[i] < 0 ? 0.f : 1.f / sum[i];
-                uint16_t* out = a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D;
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    *reinterpret_cast<uint32_t*>(out + 8 * d + 2 * t) = pack2(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
-                if (a.lse && t == 0)
-                    a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] =
-                        pos[i] < 0 ? kNegInf : (mx[i] + (log2f(sum[i]) - kUp)) * 0.6931471805599453f;
             }
         }
         first_segment = false;
@@ -610,8 +732,6 @@ cudaError_t layer_map(CUtensorMap& map, EncodeFn fn, const KvArgs& c, uint16_t* 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-constexpr int kMaxCtas = 148 * 2;
-
 // Rows per tile: the smallest that holds a (sequence, head)'s rows, up to 64.
 int attn_tile_rows(int m, int group)
 {
@@ -647,7 +767,7 @@ cudaError_t launch_attn_t(const AttnArgs& a, cudaStream_t stream)
 size_t attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim)
 {
     const int rows = attn_tile_rows(m, n_q_heads / n_heads);
-    return ws_data_off() + align_up(sizeof(float) * 2 * (size_t)kMaxCtas * rows * (head_dim + 2), 256);
+    return ws_data_off() + align_up(sizeof(float) * 2 * (size_t)kMaxCtas * rows * (head_dim + 4), 256);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream)

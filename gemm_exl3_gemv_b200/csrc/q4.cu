@@ -4,34 +4,44 @@
 //     y[i][n] = sum_k x[i][k] (q[k][n] - z[k/g][n]) s[k/g][n],   1..32 rows
 //
 // The product reads half a byte per weight and does 2 m flops with it, so at
-// few rows the stream of packed words is the bound.  What a weight may cost
-// in instructions at that rate is about three; the kernel spends a little
-// over one:
+// few rows the stream of packed words is the bound, if a weight costs less
+// than about three instruction slots (148 SMs x 128 lanes at 1.9 GHz against
+// 13e12 weights a second).  At 17..32 rows the legacy tensor pipe's rate
+// (0.92 mma.m16n8k16 per ns and SM measured) is about as tight a bound.
 //   * The packed tiles (16 channels x 64 inputs, layout in include/exl3.h) are
 //     the A operand of mma.m16n8k16 in register order: a lane's 128-bit load
-//     is its share of four k-steps.  Two fields of a word become an fp16 pair
-//     by one OR into the mantissa of 1024 (fields at bits 0 and 16) or of
-//     1024 again with the field worth 16 (bits 4 and 20), and one packed add
-//     or FMA takes the bias and the zero point off.  Both are exact: |q - z|
-//     is an integer below 2048, for any uint8 zero.
-//   * x is the B operand straight from global memory (the few rows live in
-//     L1): a lane reads 8 consecutive inputs of its row per 32-input block.
+//     is its share of four k-steps, and two fields of a word become an fp16
+//     pair by one AND with a mask.
+//     Up to 8 rows the masked fields are the operand: as fp16 bits they are
+//     the subnormals q 2^-24 (fields at bits 0 and 16) and q 2^-20 (bits 4 and
+//     20), which the tensor cores take exactly; the zero point is taken off
+//     the group's sum, with sum(x) from one more mma of ones.
+//     For more rows the zero point is taken off the operand, (q - z) in
+//     integers below 2048, exact in fp16: that costs four packed adds a word,
+//     and saves the mma of ones and the second FMA of every sum.
+//   * Words, scales, zero points and x come by asynchronous copies through
+//     rings in shared memory: a warp's own for the weights, one shared by the
+//     warps that work on the same inputs for x, whose B fragments are 128-bit
+//     reads.  (Bulk copies of such small pieces were slower: an SM started one
+//     in about 22 ns, and a step needs two to forty of them.)
 //   * The fp32 sums of a group are scaled in fp32 and added up; nothing is
 //     rounded below 32 bits before the result.
-// A warp takes a run of 64-input tiles of 16*CT channels; the warps of a CTA
-// and the CTAs of a cut (grid.y) split the inputs.  Sums are joined in warp
-// order in shared memory, and in CTA order by the last CTA to arrive.
+// A warp takes steps of 128 inputs of 16*CT channels; some of a CTA's 8 warps lie
+// along the channels, the others along the inputs, and the CTAs of a cut
+// (grid.y) split the inputs.  Sums are joined in warp order in shared memory,
+// and in CTA order by the last CTA to arrive.
 #include <cuda_fp16.h>
 
-#include "exl3_common.cuh"
+#include <type_traits>
+
 #include "exl3_internal.h"
+#include "exl3_tc.cuh"
 
 namespace exl3 {
 
 namespace {
 
-constexpr int kQ4Warps = 8;
-constexpr int kQ4Threads = 32 * kQ4Warps;
+constexpr int kQ4MaxDepth = 5;
 
 struct Q4Args {
     const uint16_t* x;
@@ -40,7 +50,9 @@ struct Q4Args {
     const uint8_t* zero;
     void* y;
     int m, k_in, n_out, y_fp32;
+    int warps_c;              // warps of a CTA along the channels (a power of two; the others along the inputs)
     int splits;               // CTAs that share a channel block's inputs
+    int depth;                // stages of the rings
     unsigned char* ws;
 };
 
@@ -49,41 +61,190 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cas
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The A fragment of one k-step: rows g (lo) and g + 8 (hi) of the tile.
-// zlo = -(1024 + z) and zhi = -(64 + z) as pairs.
-__device__ __forceinline__ void q4_fragment(uint32_t w, __half2 zlo, __half2 zhi, uint32_t (&a)[4])
+// The same into a sum that starts at zero.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-    const uint32_t v = w >> 8;
-    a[0] = h2_bits(__hadd2(bits_h2((w & 0x000F000Fu) | 0x64006400u), zlo));
-    a[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, zhi));
-    a[2] = h2_bits(__hadd2(bits_h2((v & 0x000F000Fu) | 0x64006400u), zlo));
-    a[3] = h2_bits(__hfma2(bits_h2((v & 0x00F000F0u) | 0x64006400u), sixteenth, zhi));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-template <int CT, int NT, int GROUP>
-__global__ void __launch_bounds__(kQ4Threads) q4_gemm_kernel(Q4Args p)
+// The pair's fields in the mantissa of 1024, in one instruction.
+__device__ __forceinline__ __half2 masked_1024(uint32_t w, uint32_t mask)
 {
-    constexpr int kBlockCh = 16 * CT;
-    constexpr int kRows = 8 * NT;
-    extern __shared__ __align__(16) float red[];            // warps x channels x rows
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return bits_h2(r);
+}
+
+// The A fragment of one k-step: rows g (a0, a2) and g + 8 (a1, a3) of the tile.
+// RAW: the fields as subnormals, 2^-24 and 2^-20 of their values.  Otherwise
+// q - z from 1024 + q and 1024 + 16 q: zlo = -(1024 + z), zhi = -(64 + z).
+template <bool RAW>
+__device__ __forceinline__ void q4_fragment(uint32_t w, __half2 zlo, __half2 zhi, uint32_t (&a)[4])
+{
+    const uint32_t v = w >> 8;
+    if constexpr (RAW) {
+        a[0] = w & 0x000F000Fu;
+        a[1] = w & 0x00F000F0u;
+        a[2] = v & 0x000F000Fu;
+        a[3] = v & 0x00F000F0u;
+    } else {
+        const __half2 sixteenth = __float2half2_rn(0.0625f);
+        a[0] = h2_bits(__hadd2(masked_1024(w, 0x000F000Fu), zlo));
+        a[1] = h2_bits(__hfma2(masked_1024(w, 0x00F000F0u), sixteenth, zhi));
+        a[2] = h2_bits(__hadd2(masked_1024(v, 0x000F000Fu), zlo));
+        a[3] = h2_bits(__hfma2(masked_1024(v, 0x00F000F0u), sixteenth, zhi));
+    }
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Reads from shared memory by 32-bit address, so that the compiler adds no
+// 64-bit arithmetic to them.
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float lds_half(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    return __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ uint32_t lds_byte(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+// All but the last n groups of this thread's copies have landed.
+__device__ __forceinline__ void cp_async_wait(int n)
+{
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// CT: channel tiles of a warp.  NT: row tiles (of 8).  SPS: steps (of 128
+// inputs) that a stage of the rings holds.
+template <int CT, int NT, int SPS, int GROUP>
+struct Q4Shape {
+    static constexpr int kWarps = 8, kThreads = 32 * kWarps;
+    static constexpr int kParts = 128 / GROUP;               // groups of a step
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kScales = SPS * CT * 1024;          // where a stage's scales and zero points lie: per group
+    static constexpr int kZeros = kScales + SPS * kParts * CT * 32;
+    static constexpr int kStage = kZeros + SPS * kParts * CT * 16;
+    static constexpr int kXRow = SPS * 256 + 64;             // bytes from row to row of x: 8 lanes' reads meet no bank twice
+    static constexpr int kMinCtas = 2;                       // per SM
+};
+
+template <int CT, int NT, int SPS, int GROUP>
+__global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) q4_gemm_kernel(const __grid_constant__ Q4Args p)
+{
+    using S = Q4Shape<CT, NT, SPS, GROUP>;
+    constexpr bool kRaw = NT == 1;
+    constexpr int kParts = S::kParts;
+    extern __shared__ __align__(128) unsigned char smem[];
+    float* red = reinterpret_cast<float*>(smem);             // after the loop: inputs' warps x rows x channels
     __shared__ int last_flag;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+    const int wc = warp & (p.warps_c - 1), wk = warp / p.warps_c, warps_k = S::kWarps / p.warps_c;
     const int g = lane >> 2, t = lane & 3;
-    const int kt_all = p.k_in / 64;
-    const int tn0 = blockIdx.x * CT, tn_all = p.n_out / 16;
-    const int slice = blockIdx.y * kQ4Warps + warp, slices = p.splits * kQ4Warps;
-    const int kt0 = (int)((long long)kt_all * slice / slices), kt1 = (int)((long long)kt_all * (slice + 1) / slices);
-
+    const int kt_all = p.k_in / 64, tn_all = p.n_out / 16, steps = (kt_all + 1) / 2;
+    const int tn0 = (blockIdx.x * p.warps_c + wc) * CT;
+    const int tiles = max(0, min(CT, tn_all - tn0));         // of this warp; the last CTA's may have none
+    const int slice = blockIdx.y * warps_k + wk, slices = p.splits * warps_k;
+    const int s0 = (int)((long long)steps * slice / slices), s1 = (int)((long long)steps * (slice + 1) / slices);
+    const int depth = p.depth;
+    unsigned char* ring = smem + warp * depth * S::kStage;
+    unsigned char* x_ring = smem + S::kWarps * depth * S::kStage + wk * depth * (p.m * S::kXRow);
+    if (!p.zero)                                             // no copy comes there
+        for (int i = 0; i < depth; ++i)
+            for (int j = 4 * lane; j < S::kStage - S::kZeros; j += 128)
+                *reinterpret_cast<uint32_t*>(ring + i * S::kStage + S::kZeros + j) = 0x08080808u;
     grid_dep_wait();
     grid_dep_launch();
+
+    // The copies of a stage (steps s .. s + SPS - 1, as far as they belong to
+    // this slice): 512 bytes a tile of words; scales (2 pieces of 16 bytes a
+    // tile) and zero points (1 piece), a group each; and this warp's part of
+    // the rows of x.  k_in ends on half a step if it is no multiple of 128.
+    // Every lane's sources advance by the same distance from stage to stage.
+    const int kt_end = min(2 * s1, kt_all);
+    const uint4* words[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+        words[c] = reinterpret_cast<const uint4*>(p.packed) + ((long long)min(tn0 + c, tn_all - 1) * kt_all + 2 * s0) * 32 + lane;
+    constexpr int kPieces = 3 * CT, kGroupPieces = SPS * kParts * kPieces, kMine = (kGroupPieces + 31) / 32;
+    const unsigned char* piece[kMine];
+    uint32_t piece_to[kMine];
+    int piece_step[kMine], piece_group[kMine];               // group: past every k_in where there is none
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = lane + 32 * j, part = i / kPieces, r = i % kPieces;
+        const long long at = (long long)(s0 * kParts + part) * p.n_out + 16 * tn0;
+        const bool is_zero = r >= 2 * CT;
+        piece[j] = is_zero ? p.zero + at + 16 * (r - 2 * CT) : reinterpret_cast<const unsigned char*>(p.scale + at + 8 * r);
+        piece_to[j] = is_zero ? S::kZeros + part * (CT * 16) + (r - 2 * CT) * 16 : S::kScales + part * (CT * 32) + r * 16;
+        piece_step[j] = SPS * kParts * p.n_out * (is_zero ? 1 : 2);
+        piece_group[j] = i < kGroupPieces && (is_zero ? p.zero && r - 2 * CT < tiles : r < 2 * tiles) ? s0 * kParts + part : 1 << 30;
+    }
+    const int group_end = min(s1 * kParts, p.k_in / GROUP);
+    // x: kCols threads along the inputs, the others of the warps that share it along the rows
+    constexpr int kXPieces = SPS * 16;                       // of a row
+    const int x_threads = 32 * p.warps_c, x_lane = wc * 32 + lane;
+    const int x_cols = min(x_threads, kXPieces), x_rows = x_threads / x_cols, x_row = x_lane / x_cols, x_col = x_lane % x_cols;
+    const uint16_t* x_from = p.x + (long long)x_row * p.k_in + 128 * s0 + 8 * x_col;
+    const uint32_t x_to = smem_u32(x_ring) + x_row * S::kXRow + 16 * x_col;
+    const long long x_next = (long long)x_rows * p.k_in;
+    int fetched = s0;                                        // steps
+    auto fetch = [&](int stage) {
+        const uint32_t to = smem_u32(ring) + stage * S::kStage;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+#pragma unroll
+            for (int i = 0; i < 2 * SPS; ++i)
+                if (2 * fetched + i < kt_end) copy16(to + c * (SPS * 1024) + i * 512 + lane * 16, words[c] + i * 32);
+            words[c] += SPS * 64;
+        }
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            if (piece_group[j] < group_end) copy16(to + piece_to[j], piece[j]);
+            piece[j] += piece_step[j];
+            piece_group[j] += SPS * kParts;
+        }
+        const uint32_t xt = x_to + stage * p.m * S::kXRow;
+        for (int col = 0; col < kXPieces; col += x_cols) {
+            if (128 * fetched + 8 * (x_col + col) >= 64 * kt_end) break;
+            const uint16_t* src = x_from + 8 * col;
+            uint32_t dst = xt + 16 * col;
+            for (int row = x_row; row < p.m; row += x_rows, src += x_next, dst += x_rows * S::kXRow) copy16(dst, src);
+        }
+        x_from += SPS * 128;
+        fetched += SPS;
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    for (int i = 0; i < depth - 1; ++i) {
+        if (fetched < s1) fetch(i);
+        commit();
+    }
 
     float acc[CT][NT][4];
 #pragma unroll
@@ -92,105 +253,164 @@ __global__ void __launch_bounds__(kQ4Threads) q4_gemm_kernel(Q4Args p)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.f;
+    // columns past the last row repeat it; their sums are not written
+    int row_at[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) row_at[n] = min(8 * n + g, p.m - 1) * S::kXRow + 16 * t;
 
-    for (int kt = kt0; kt < kt1; ++kt) {
+    float sum[CT][NT][4], xs[4];
+    __half2 zlo[CT], zhi[CT];
+    // 64 inputs (the first or second tile of a step) from shared memory
+    auto tile = [&](auto second, uint32_t words_at, const uint32_t (&x_at)[NT], uint32_t scales, uint32_t zeros) {
+        constexpr int kSecond = decltype(second)::value;
         uint4 w[CT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int tn = min(tn0 + c, tn_all - 1);
-            w[c] = __ldg(reinterpret_cast<const uint4*>(p.packed) + ((long long)tn * kt_all + kt) * 32 + lane);
-        }
-        uint4 b[NT][2];
+        for (int c = 0; c < CT; ++c) w[c] = lds16(words_at + c * (SPS * 1024) + kSecond * 512);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = 8 * n + g;
+        for (int half = 0; half < 2; ++half) {               // 32 inputs
+            const int k = 64 * kSecond + 32 * half, part = k / GROUP;
+            const bool opens = k % GROUP == 0, closes = (k + 32) % GROUP == 0;
+            if (!kRaw && opens) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                b[n][h] = row < p.m ? *reinterpret_cast<const uint4*>(p.x + (long long)row * p.k_in + 64 * kt + 32 * h + 8 * t)
-                                    : make_uint4(0, 0, 0, 0);
-        }
+                for (int c = 0; c < CT; ++c) {
+                    const int ch = (part * CT + c) * 16;
+                    // -(1024 + z) is the bits of -1024 with z in the last places; -(64 + z) is 960 more
+                    zlo[c] = bits_h2(0xE400E400u | lds_byte(zeros + ch) * 0x10001u);
+                    zhi[c] = __hadd2(bits_h2(0xE400E400u | lds_byte(zeros + ch + 8) * 0x10001u), __float2half2_rn(960.f));
+                }
+            }
+            uint4 x[NT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int ch = 16 * min(tn0 + c, tn_all - 1) + g;
-            const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-            constexpr int kParts = GROUP == 32 ? 2 : 1;      // groups inside the 64 inputs
+            for (int n = 0; n < NT; ++n) x[n] = lds16(x_at[n] + 128 * kSecond + 64 * half);
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-                const long long at = (long long)((64 * kt) / GROUP + part) * p.n_out + ch;
-                const float s_lo = __half2float(__ushort_as_half(p.scale[at]));
-                const float s_hi = __half2float(__ushort_as_half(p.scale[at + 8]));
-                const int z_lo = p.zero ? p.zero[at] : 8, z_hi = p.zero ? p.zero[at + 8] : 8;
-                const __half2 zlo = __half2half2(__int2half_rn(-1024 - z_lo)), zhi = __half2half2(__int2half_rn(-64 - z_hi));
-                float sum[NT][4];
+            for (int i = 0; i < 2; ++i) {                    // k-steps of 16 inputs
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
-#pragma unroll
-                for (int j = part * (4 / kParts); j < (part + 1) * (4 / kParts); ++j) {
+                for (int c = 0; c < CT; ++c) {
                     uint32_t a[4];
-                    q4_fragment(words[j], zlo, zhi, a);
+                    q4_fragment<kRaw>(half ? (i ? w[c].w : w[c].z) : (i ? w[c].y : w[c].x), zlo[c], zhi[c], a);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint4 bb = b[n][j >> 1];
-                        if (j & 1) mma_16816(sum[n], a, bb.z, bb.w);
-                        else mma_16816(sum[n], a, bb.x, bb.y);
+                        const uint32_t b0 = i ? x[n].z : x[n].x, b1 = i ? x[n].w : x[n].y;
+                        if (opens && i == 0) mma_16816_first(sum[c][n], a, b0, b1);
+                        else mma_16816(sum[c][n], a, b0, b1);
                     }
                 }
+                if constexpr (kRaw) {
+                    const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+                    const uint32_t b0 = i ? x[0].z : x[0].x, b1 = i ? x[0].w : x[0].y;
+                    if (opens && i == 0) mma_16816_first(xs, ones, b0, b1);
+                    else mma_16816(xs, ones, b0, b1);
+                }
+            }
+            if (closes) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[c][n][0] += s_lo * sum[n][0];
-                    acc[c][n][1] += s_lo * sum[n][1];
-                    acc[c][n][2] += s_hi * sum[n][2];
-                    acc[c][n][3] += s_hi * sum[n][3];
+                for (int c = 0; c < CT; ++c) {
+                    const int ch = (part * CT + c) * 16;
+                    float s_lo = lds_half(scales + 2 * ch), s_hi = lds_half(scales + 2 * ch + 16);
+                    if constexpr (kRaw) {
+                        // a byte in the last places of 2^23, less 2^23
+                        const float z_lo = (__uint_as_float(0x4B000000u | lds_byte(zeros + ch)) - 8388608.f) * 0x1p-24f;
+                        const float z_hi = (__uint_as_float(0x4B000000u | lds_byte(zeros + ch + 8)) - 8388608.f) * 0x1p-20f;
+                        s_lo *= 0x1p24f;
+                        s_hi *= 0x1p20f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[c][0][e] -= (e < 2 ? z_lo : z_hi) * xs[e];
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[c][n][e] += (e < 2 ? s_lo : s_hi) * sum[c][n][e];
                 }
             }
         }
+    };
+
+    int stage = 0;
+    for (int s = s0; s < s1; s += SPS) {
+        // this stage has landed, for every warp that shares its rows, and the
+        // one before it is read
+        cp_async_wait(depth - 2);
+        if (p.warps_c == 1) __syncwarp();
+        else named_bar(1 + wk, x_threads);
+        if (fetched < s1) fetch(stage == 0 ? depth - 1 : stage - 1);
+        commit();
+        const uint32_t at = smem_u32(ring) + stage * S::kStage;
+        uint32_t words_at = at + lane * 16, scales = at + S::kScales + 2 * g, zeros = at + S::kZeros + g, x_at[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x_at[n] = smem_u32(x_ring) + stage * p.m * S::kXRow + row_at[n];
+        const int here = min(SPS, s1 - s);
+#pragma unroll 1
+        for (int i = 0; i < here; ++i) {
+            tile(std::integral_constant<int, 0>{}, words_at, x_at, scales, zeros);
+            if (2 * (s + i) + 1 < kt_all) tile(std::integral_constant<int, 1>{}, words_at, x_at, scales, zeros);
+            words_at += 1024;
+            scales += kParts * CT * 32;
+            zeros += kParts * CT * 16;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x_at[n] += 256;
+        }
+        if (++stage == depth) stage = 0;
     }
 
-    // join the warps: red[warp][row][channel]
+    // join the warps along the inputs: red[wk][row][channel]
+    const int ch_cta = 16 * CT * p.warps_c;
+    __syncthreads();                                         // the rings are read
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int row = 8 * n + 2 * t + (e & 1), ch = 16 * c + g + 8 * (e >> 1);
-                red[(warp * kRows + row) * kBlockCh + ch] = acc[c][n][e];
+                const int row = 8 * n + 2 * t + (e & 1), ch = 16 * (CT * wc + c) + g + 8 * (e >> 1);
+                red[(wk * S::kRows + row) * ch_cta + ch] = acc[c][n][e];
             }
     __syncthreads();
-    const int ch_here = min(kBlockCh, p.n_out - tn0 * 16);
-    float* part = reinterpret_cast<float*>(p.ws + ws_data_off()) +
-                  (size_t)(blockIdx.x * p.splits) * (kBlockCh * p.m);
-    for (int i = threadIdx.x; i < p.m * kBlockCh; i += kQ4Threads) {
-        float s = red[i];
-#pragma unroll
-        for (int v = 1; v < kQ4Warps; ++v) s += red[v * kRows * kBlockCh + i];
-        red[i] = s;
-        if (p.splits > 1) part[(size_t)blockIdx.y * (kBlockCh * p.m) + i] = s;
+    const int row_vecs = ch_cta / 4, vecs = p.m * row_vecs;  // four channels at a time
+    float4* red4 = reinterpret_cast<float4*>(smem);
+    float4* part4 = reinterpret_cast<float4*>(p.ws + ws_data_off()) + (size_t)blockIdx.x * p.splits * vecs;
+    for (int i = threadIdx.x; i < vecs; i += S::kThreads) {
+        float4 s = red4[i];
+        for (int v = 1; v < warps_k; ++v) {
+            const float4 o = red4[v * (S::kRows * row_vecs) + i];
+            s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+        }
+        if (p.splits > 1) __stcg(part4 + (size_t)blockIdx.y * vecs + i, s);
+        else red4[i] = s;
     }
     if (p.splits > 1) {
         __threadfence();
         __syncthreads();
         uint32_t* counter = reinterpret_cast<uint32_t*>(p.ws + ws_counter_off()) + blockIdx.x;
-        if (threadIdx.x == 0) last_flag = atomicAdd(counter, 1u) == (uint32_t)p.splits - 1;
+        if (threadIdx.x == 0) {
+            last_flag = atomicAdd(counter, 1u) == (uint32_t)p.splits - 1;
+            if (last_flag) *counter = 0;
+        }
         __syncthreads();
         if (!last_flag) return;
-        if (threadIdx.x == 0) *counter = 0;
         __threadfence();
-        for (int i = threadIdx.x; i < p.m * kBlockCh; i += kQ4Threads) {
-            float s = 0.f;
-            for (int v = 0; v < p.splits; ++v) s += __ldcg(part + (size_t)v * (kBlockCh * p.m) + i);
-            red[i] = s;
-        }
     }
-    // every thread reads back what it wrote itself: no barrier is needed
-    for (int i = threadIdx.x; i < p.m * kBlockCh; i += kQ4Threads) {
-        const int row = i / kBlockCh, ch = i % kBlockCh;
+    const int ch_here = min(ch_cta, p.n_out - (int)blockIdx.x * ch_cta);
+    for (int i = threadIdx.x; i < vecs; i += S::kThreads) {
+        const int row = i / row_vecs, ch = 4 * (i % row_vecs);
         if (ch >= ch_here) continue;
-        const long long at = (long long)row * p.n_out + tn0 * 16 + ch;
-        if (p.y_fp32) static_cast<float*>(p.y)[at] = red[i];
-        else static_cast<__half*>(p.y)[at] = __float2half_rn(red[i]);
+        float4 s;
+        if (p.splits > 1) {
+            s = __ldcg(part4 + i);
+#pragma unroll 4
+            for (int v = 1; v < p.splits; ++v) {
+                const float4 o = __ldcg(part4 + (size_t)v * vecs + i);
+                s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+            }
+        } else {
+            s = red4[i];                                     // written by this thread
+        }
+        const long long out = (long long)row * p.n_out + (long long)blockIdx.x * ch_cta + ch;
+        if (p.y_fp32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + out) = s;
+        } else {
+            const __half2 lo = __floats2half2_rn(s.x, s.y), hi = __floats2half2_rn(s.z, s.w);
+            *reinterpret_cast<uint2*>(static_cast<__half*>(p.y) + out) = make_uint2(h2_bits(lo), h2_bits(hi));
+        }
     }
 }
 
@@ -215,39 +435,61 @@ __global__ void __launch_bounds__(256) q4_pack_kernel(const uint8_t* __restrict_
     }
 }
 
+// How a product is cut.  Warps stream; what they have to be is many and long:
+// the channel tiles of all warps times the cuts of the inputs should fill the
+// GPU about once.  The cuts are first the warps of a CTA (joined in shared
+// memory), then CTAs.  With more rows, warps of a CTA rather lie along the
+// channels, so that x is read less often: a CTA then takes 8 m channels and
+// more, and x is at most half the bytes of the weights.
 struct Q4Plan {
-    int ct, nt, blocks, splits;
+    int shape, ct, rows, warps_c, blocks, splits, depth;
 };
 
 Q4Plan q4_plan(int m, int k_in, int n_out)
 {
     Q4Plan pl;
-    pl.nt = m <= 8 ? 1 : m <= 16 ? 2 : 4;
-    pl.ct = pl.nt;
-    pl.blocks = (n_out / 16 + pl.ct - 1) / pl.ct;
-    const int slots = 148 * (pl.nt == 1 ? 4 : 2);
-    int s = slots / pl.blocks;
-    const int most = (k_in / 64 + 2 * kQ4Warps - 1) / (2 * kQ4Warps);
-    if (s > most) s = most;
-    if (s < 1 || pl.blocks > kMaxBlocks) s = 1;
-    pl.splits = s;
+    pl.shape = m <= 2 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : m <= 24 ? 3 : 4;
+    pl.ct = pl.shape == 0 ? 1 : 2;
+    pl.rows = pl.shape <= 1 ? 8 : 8 * pl.shape;
+    const int steps = (k_in / 64 + 1) / 2, tiles = (n_out / 16 + pl.ct - 1) / pl.ct;
+    const int warps = 148 * 8 * 2;
+    int cuts = warps / tiles;                                // of the inputs
+    if (cuts > steps / 2) cuts = steps / 2;
+    if (cuts < 1) cuts = 1;
+    const int least_c = pl.shape == 0 ? 1 : pl.shape == 1 ? 2 : 4;
+    pl.warps_c = 8;
+    while (pl.warps_c > least_c && 16 / pl.warps_c <= cuts) pl.warps_c /= 2;
+    pl.blocks = (tiles + pl.warps_c - 1) / pl.warps_c;
+    pl.splits = cuts / (8 / pl.warps_c);
+    if (pl.splits < 1 || pl.blocks > kMaxBlocks) pl.splits = 1;
     return pl;
 }
 
-template <int CT, int NT>
-cudaError_t launch_q4_t(const Q4Args& a, const Q4Plan& pl, int group, cudaStream_t stream)
+template <int CT, int NT, int SPS, int GROUP>
+cudaError_t launch_q4_t(Q4Args a, const Q4Plan& pl, cudaStream_t stream)
 {
-    auto kern = group == 32 ? q4_gemm_kernel<CT, NT, 32>
-                            : group == 64 ? q4_gemm_kernel<CT, NT, 64> : q4_gemm_kernel<CT, NT, 128>;
-    constexpr size_t smem = sizeof(float) * kQ4Warps * 16 * CT * 8 * NT;
-    if (smem > 48 * 1024) {
-        static std::atomic<int> done[3][kMaxDevices];
-        cudaError_t e = once_per_device(done[group == 32 ? 0 : group == 64 ? 1 : 2], [&] {
-            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        });
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(kern, dim3((unsigned)pl.blocks, (unsigned)pl.splits), dim3(kQ4Threads), smem, stream, a);
+    using S = Q4Shape<CT, NT, SPS, GROUP>;
+    auto kern = q4_gemm_kernel<CT, NT, SPS, GROUP>;
+    // as many stages as fit beside kMinCtas - 1 other CTAs on an SM
+    const int stage = S::kWarps * S::kStage + S::kWarps / pl.warps_c * a.m * S::kXRow;
+    constexpr int kRoom = 227 * 1024 / S::kMinCtas - 3072;
+    a.depth = kRoom / stage;                                 // two at least: the largest stage takes half of kRoom
+    if (a.depth > kQ4MaxDepth) a.depth = kQ4MaxDepth;
+    const int join = (int)sizeof(float) * S::kWarps * 16 * CT * S::kRows;
+    const int smem = a.depth * stage > join ? a.depth * stage : join;
+    static std::atomic<int> done[kMaxDevices];
+    const cudaError_t e = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)pl.blocks, (unsigned)pl.splits), dim3(S::kThreads), (size_t)smem, stream, a);
+}
+
+template <int CT, int NT, int SPS>
+cudaError_t launch_q4_g(const Q4Args& a, const Q4Plan& pl, int group, cudaStream_t stream)
+{
+    return group == 32 ? launch_q4_t<CT, NT, SPS, 32>(a, pl, stream)
+                       : group == 64 ? launch_q4_t<CT, NT, SPS, 64>(a, pl, stream) : launch_q4_t<CT, NT, SPS, 128>(a, pl, stream);
 }
 
 }  // namespace
@@ -256,7 +498,7 @@ size_t q4_workspace_bytes(int m, int k_in, int n_out)
 {
     const Q4Plan pl = q4_plan(m, k_in, n_out);
     if (pl.splits == 1) return ws_data_off();
-    return ws_data_off() + align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * m, 256);
+    return ws_data_off() + align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256);
 }
 
 cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,
@@ -264,11 +506,13 @@ cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, con
                            unsigned char* ws, cudaStream_t stream)
 {
     const Q4Plan pl = q4_plan(m, k_in, n_out);
-    const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws};
-    switch (pl.nt) {
-        case 1: return launch_q4_t<1, 1>(a, pl, group, stream);
-        case 2: return launch_q4_t<2, 2>(a, pl, group, stream);
-        default: return launch_q4_t<4, 4>(a, pl, group, stream);
+    const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws};
+    switch (pl.shape) {
+        case 0: return launch_q4_g<1, 1, 4>(a, pl, group, stream);
+        case 1: return launch_q4_g<2, 1, 2>(a, pl, group, stream);
+        case 2: return launch_q4_g<2, 2, 2>(a, pl, group, stream);
+        case 3: return launch_q4_g<2, 3, 1>(a, pl, group, stream);
+        default: return launch_q4_g<2, 4, 1>(a, pl, group, stream);
     }
 }
 

@@ -61,7 +61,8 @@ class KvCache:
         if n == 0:
             raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"a cache of {n_pages} pages")
         self.scratch = torch.zeros(n, dtype=torch.uint8, device=k.device)
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
+        self._scale = 1.0 / math.sqrt(head_dim)
         self._desc = ex.Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                               free.data_ptr(), self.scratch.data_ptr(), n_layers, n_pages, n_heads, page_size,
                               head_dim, n_seqs, max_pages)
@@ -80,49 +81,55 @@ class KvCache:
 
     # ------------------------------------------------------------ checks ---
 
-    def _list(self, t: torch.Tensor, what: str, n: Optional[int] = None) -> int:
-        if t.dim() != 1 or t.dtype is not torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{what}: expected a contiguous one-dimensional int32 tensor")
-        if t.device != self.device:
-            raise ValueError(f"{what}: expected a tensor on {self.device}, got {t.device}")
+    def _list(self, t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[int]:
+        """Checks a list of int32 numbers (of n entries); its address, None for
+        no list."""
+        if t is None:
+            return None
+        if t.dim() != 1 or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{what}: expected a contiguous one-dimensional int32 tensor on {self.device}, got {t.dtype} "
+                             f"of shape {tuple(t.shape)} on {t.device}")
         if n is not None and t.shape[0] != n:
             raise ValueError(f"{what}: expected {n} entries, got {t.shape[0]}")
         if t.shape[0] > MAX_LIST:
             raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"{what}: a list of more than {MAX_LIST} entries")
-        return t.shape[0]
+        return t.data_ptr()
 
     def _rows(self, t: torch.Tensor, what: str, n: int, heads: int):
-        """Checks (n, m, heads, head_dim) rows, dense within a row, and returns
-        m and the strides between entries and between rows."""
-        if t.dim() != 4 or t.dtype is not torch.float16 or t.shape[0] != n or t.shape[2] != heads or \
-                t.shape[3] != self.head_dim:
-            raise ValueError(f"{what}: expected fp16 of shape ({n}, m, {heads}, {self.head_dim}), got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{what}: expected a tensor on {self.device}, got {t.device}")
-        m, (s0, s1, s2, s3) = t.shape[1], t.stride()
-        if s3 != 1 or (s2 != self.head_dim and heads > 1) or (s1 % 8 and m > 1) or (s0 % 8 and n > 1):
+        """Checks (n, m, heads, head_dim) rows, dense within a row; returns m and
+        the strides between entries and between rows."""
+        shape = t.shape
+        if len(shape) != 4 or t.dtype is not torch.float16 or shape[0] != n or shape[2] != heads or \
+                shape[3] != self.head_dim or t.get_device() != self._index:
+            raise ValueError(f"{what}: expected fp16 of shape ({n}, m, {heads}, {self.head_dim}) on {self.device}, got "
+                             f"{t.dtype} {tuple(shape)} on {t.device}")
+        m, (s0, s1, s2, s3) = shape[1], t.stride()
+        if m <= 1:
+            s1 = 0
+        if n <= 1:
+            s0 = 0
+        if s3 != 1 or (s2 != self.head_dim and heads > 1) or s1 % 8 or s0 % 8:
             raise ValueError(f"{what}: the heads of a row must lie one behind the other, rows and entries a multiple of "
                              f"8 elements apart; strides are {t.stride()}")
-        return m, (s0 if n > 1 else 0), (s1 if m > 1 else 0)
+        return m, s0, s1
 
-    def _here(self):
-        if torch.cuda.current_device() != self.device.index:
+    def _where(self, stream):
+        """The stream's handle; the cache's device must be the current one."""
+        if torch.cuda.current_device() != self._index:
             raise ValueError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        return ex._raw_stream(self._index) if stream is None else stream.cuda_stream
 
     # ------------------------------------------------------- bookkeeping ---
 
     def reset(self, stream=None):
         """No sequence holds anything, every page is free."""
-        self._here()
-        ex._check(ex.lib.exl3_kv_reset(self._ref, ex._stream(stream)), "exl3_kv_reset")
+        ex._check(ex.lib.exl3_kv_reset(self._ref, self._where(stream)), "exl3_kv_reset")
 
     def status(self, stream=None) -> int:
         """Synchronises, then reads and clears the fault word: EXL3_OK,
         EXL3_ERR_CACHE_FULL or EXL3_ERR_INDEX.  While it is set, ``extend``
         and ``write`` do nothing."""
-        self._here()
-        return int(ex.lib.exl3_kv_status(self._ref, ex._stream(stream)))
+        return int(ex.lib.exl3_kv_status(self._ref, self._where(stream)))
 
     def check(self, stream=None):
         """``status()`` as an exception."""
@@ -131,52 +138,43 @@ class KvCache:
     def extend(self, seqs: torch.Tensor, m: int, counts: Optional[torch.Tensor] = None, stream=None):
         """Each sequence of ``seqs`` grows by ``m`` tokens (counts: by
         counts[b], 0..m), whose keys and values ``write`` then brings."""
-        n = self._list(seqs, "seqs")
-        if counts is not None:
-            self._list(counts, "counts", n)
-        self._here()
+        p, n = self._list(seqs, "seqs"), seqs.shape[0]
+        c, s = self._list(counts, "counts", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_extend(self._ref, n, m, seqs.data_ptr(), None if counts is None else counts.data_ptr(),
-                                            ex._stream(stream)), "exl3_kv_extend")
+            ex._check(ex.lib.exl3_kv_extend(self._ref, n, m, p, c, s), "exl3_kv_extend")
 
     def write(self, layer: int, seqs: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               counts: Optional[torch.Tensor] = None, stream=None):
         """Keys and values (n, m, n_heads, head_dim) of the last m (counts:
         counts[b]) tokens of each sequence, in one layer."""
-        n = self._list(seqs, "seqs")
-        if counts is not None:
-            self._list(counts, "counts", n)
-        m, bs, rs = self._rows(k, "k", n, self.n_heads)
-        if self._rows(v, "v", n, self.n_heads) != (m, bs, rs):
+        p, n = self._list(seqs, "seqs"), seqs.shape[0]
+        c = self._list(counts, "counts", n)
+        rows = self._rows(k, "k", n, self.n_heads)
+        if self._rows(v, "v", n, self.n_heads) != rows:
             raise ValueError("k and v must have the same shape and strides")
-        self._here()
+        m, bs, rs = rows
+        s = self._where(stream)
         if n and m:
-            ex._check(ex.lib.exl3_kv_write(self._ref, layer, n, m, seqs.data_ptr(),
-                                           None if counts is None else counts.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                           bs, rs, ex._stream(stream)), "exl3_kv_write")
+            ex._check(ex.lib.exl3_kv_write(self._ref, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s),
+                      "exl3_kv_write")
 
     def truncate(self, seqs: torch.Tensor, lens: Optional[torch.Tensor] = None, stream=None):
         """Each sequence keeps its first lens[b] tokens (None: it is freed)."""
-        n = self._list(seqs, "seqs")
-        if lens is not None:
-            self._list(lens, "lens", n)
-        self._here()
+        p, n = self._list(seqs, "seqs"), seqs.shape[0]
+        c, s = self._list(lens, "lens", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_truncate(self._ref, n, seqs.data_ptr(), None if lens is None else lens.data_ptr(),
-                                              ex._stream(stream)), "exl3_kv_truncate")
+            ex._check(ex.lib.exl3_kv_truncate(self._ref, n, p, c, s), "exl3_kv_truncate")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Each empty sequence dst[b] shares all of src[b] from now on."""
-        n = self._list(src, "src")
-        self._list(dst, "dst", n)
-        self._here()
+        p, n = self._list(src, "src"), src.shape[0]
+        d, s = self._list(dst, "dst", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_fork(self._ref, n, src.data_ptr(), dst.data_ptr(), ex._stream(stream)), "exl3_kv_fork")
+            ex._check(ex.lib.exl3_kv_fork(self._ref, n, p, d, s), "exl3_kv_fork")
 
     def compact(self, stream=None):
         """Moves pages so that the used ones are the first of the pool."""
-        self._here()
-        ex._check(ex.lib.exl3_kv_compact(self._ref, ex._stream(stream)), "exl3_kv_compact")
+        ex._check(ex.lib.exl3_kv_compact(self._ref, self._where(stream)), "exl3_kv_compact")
 
     # --------------------------------------------------------- attention ---
 
@@ -201,9 +199,8 @@ class KvCache:
         default.  lse: (n, m, n_q_heads) fp32, filled with the logarithms of
         the softmax sums.  Rows from counts[b] on are left as they were (in an
         ``out`` made here: zero)."""
-        n = self._list(seqs, "seqs")
-        if counts is not None:
-            self._list(counts, "counts", n)
+        p, n = self._list(seqs, "seqs"), seqs.shape[0]
+        c = self._list(counts, "counts", n)
         heads = q.shape[2] if q.dim() == 4 else 0
         m, qb, qr = self._rows(q, "q", n, heads)
         if out is None:
@@ -213,16 +210,14 @@ class KvCache:
         if mo != m:
             raise ValueError(f"out: expected {m} rows per sequence, got {mo}")
         if lse is not None:
-            ex._expect(lse, "lse", torch.float32, (n, m, heads))
-        self._here()
+            ex._expect(lse, "lse", torch.float32, (n, m, heads), self._index)
+        s = self._where(stream)
         if n == 0 or m == 0:
             return out
         if workspace is None:
             workspace = self.attention_workspace(n, m, heads)
-        ws_bytes = ex._room(workspace, 0)
         ex._check(ex.lib.exl3_paged_attention(
-            self._ref, layer, n, m, seqs.data_ptr(), None if counts is None else counts.data_ptr(), q.data_ptr(), qb, qr,
-            heads, 1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, sinks, out.data_ptr(), ob, orow,
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), ws_bytes, ex._stream(stream)),
-            "exl3_paged_attention")
+            self._ref, layer, n, m, p, c, q.data_ptr(), qb, qr, heads, self._scale if scale is None else scale, window,
+            sinks, out.data_ptr(), ob, orow, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            ex._room(workspace, self._index), s), "exl3_paged_attention")
         return out
