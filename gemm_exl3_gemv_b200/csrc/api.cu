@@ -603,11 +603,6 @@ extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int
     if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || q_batch_stride % 8 || q_row_stride % 8 ||
         out_batch_stride % 8 || out_row_stride % 8)
         return EXL3_ERR_MISALIGNED;
-    if (!workspace || ws_bytes < exl3_paged_attention_workspace_bytes(m, n_q_heads, t.c.n_heads, t.c.head_dim))
-        return EXL3_ERR_WORKSPACE;
-    if (!aligned256(workspace)) return EXL3_ERR_MISALIGNED;
-    st = check_arch();
-    if (st != EXL3_OK) return st;
     t.layer = layer;
     t.n = n;
     t.m = m;
@@ -626,5 +621,11 @@ extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int
     t.o_rs = out_row_stride;
     t.lse = lse;
     t.ws = static_cast<unsigned char*>(workspace);
+    if (!exl3::attention_tiles_ok(t)) return EXL3_ERR_UNSUPPORTED;
+    if (!workspace || ws_bytes < exl3_paged_attention_workspace_bytes(m, n_q_heads, t.c.n_heads, t.c.head_dim))
+        return EXL3_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return EXL3_ERR_MISALIGNED;
+    st = check_arch();
+    if (st != EXL3_OK) return st;
     return cuda_status(exl3::launch_paged_attention(t, static_cast<cudaStream_t>(stream)));
 }

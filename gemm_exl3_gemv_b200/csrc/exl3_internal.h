@@ -223,6 +223,7 @@ struct AttnArgs {
     unsigned char* ws;
 };
 size_t attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
+bool attention_tiles_ok(const AttnArgs& a);   // tiles are counted in 32 bits
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace exl3

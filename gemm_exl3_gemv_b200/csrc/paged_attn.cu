@@ -11,21 +11,30 @@
 //     tiles of all groups, in order, are cut into equal contiguous ranges, one
 //     per CTA, so the lengths may be as ragged as they like.  The cut is worked
 //     out on the device from the lengths.
-//   * A producer warp brings the tiles to shared memory with TMA (one box per
-//     page part and 64 columns, 128-byte swizzle) through a ring; consumer
-//     warps run mma.m16n8k16 on them.  The scores stay in registers: running
-//     maximum and sum in fp32, probabilities rounded to fp16 as the operand of
-//     the second product.
-//   * WR warps lie along the rows, WT along the tokens of a tile: with 16 rows
-//     or fewer four warps take 16 tokens each and are joined at the end.
+//   * A producer warp walks the CTA's range.  It brings queries and tiles to
+//     shared memory (TMA, one box per page part and 64 columns, 128-byte
+//     swizzle, through a ring) and tells the consumers what each stretch of
+//     tiles is: with the memory saturated a dependent read costs 2 us, and the
+//     producer makes them while earlier tiles are worked on.
+//   * WR warps lie along the rows.  With 64 rows or fewer, WT warps share 16
+//     rows: each takes some of the tile's tokens for the scores and, after the
+//     row maxima and the probabilities went through shared memory, some of the
+//     columns of the result, so that nothing has to be joined but sums.
+//   * mma.m16n8k16 for both products; running maximum and sum in fp32,
+//     probabilities rounded to fp16 as the operand of the second product.
 //   * A group that several CTAs share is joined by the last of them to arrive,
-//     in CTA order.
+//     in the order of the ranges, in two levels when they are many.
+// (Ranges that CTAs take as they get done were measured too: the equal shares
+// of a 131077-token sequence are done between 66 and 100 us, but each further
+// stretch cost more than the even finish gave.)
 // Masks.  Tokens past a row's position, outside its window or past the end of
 // the sequence must not matter whatever memory holds there.  Scores are
 // replaced (not added to); values that no row of the tile sees are cleared in
-// the operand; a value that only some rows see and that is not finite goes
-// through a separate path that keeps the rows apart.
+// shared memory; and values that only some rows see and that are not finite are
+// left out of the second product and added to the rows that see them.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "exl3_internal.h"
 #include "exl3_tc.cuh"
@@ -40,8 +49,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // o): the largest is 2^14, and what is 2^-28 of it is still a normal number.
 constexpr float kUp = 14.f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Tiles per CTA from which another CTA is worth its part of the join.
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 4;                                 // of a CTA's share, from which another CTA is worth its part of the join
 constexpr int kFan = 8;                                      // parts joined at once
 constexpr int kMaxCtas = 148 * 2;
 
@@ -50,6 +58,24 @@ struct AttnPlan {
     int entries;              // sequences x row tiles
     int page_shift;
     float scale_log2;
+};
+
+// How the tiles of all groups are cut: the first `more` ranges have one tile
+// more than `share`.
+struct AttnCut {
+    int ranges, share, more;
+    __device__ __forceinline__ AttnCut(int total, int ctas)
+    {
+        ranges = min(ctas, (total + kMinTiles - 1) / kMinTiles);
+        share = total / ranges;
+        more = total - share * ranges;
+    }
+    __device__ __forceinline__ int first(int r) const { return r * share + min(r, more); }
+    __device__ __forceinline__ int range_of(int tile) const
+    {
+        const int border = more * (share + 1);
+        return tile < border ? tile / (share + 1) : more + (tile - border) / share;
+    }
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -127,10 +153,13 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, const AttnPlan& pl,
 
 __device__ __forceinline__ int tile_at(const Entry& e, int i) { return i < e.sink_tiles ? i : e.tile0 + i - e.sink_tiles; }
 
-__device__ __forceinline__ int cta_of_unit(long long u, long long p, long long total)
-{
-    return (int)(((u + 1) * p - 1) / total);
-}
+// What the producer tells the consumers: the next stretch is n tiles from tile
+// off on of head h of an entry, whose group's first tile is gstart.  n = 0:
+// there are no more.
+struct Stretch {
+    Entry en;
+    int b, h, n, off, gstart, first;     // first: the first of this CTA's stretches
+};
 
 template <int D, int WR, int WT>
 struct AttnShape {
@@ -138,10 +167,17 @@ struct AttnShape {
     static constexpr int kThreads = kConsumers + 32;
     static constexpr int kRows = 16 * WR;
     static constexpr int kHalf = kTile * D * 2;              // bytes of a tile's keys (or values)
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    // shared memory for joining the warps, and the statistics of joined parts
-    static constexpr int kJoin = WT > 1 ? (WT / 2) * kRows * (D + 2) * 4 : (kConsumers + kRows) * 8;
-    static constexpr int kSmem = kStages * 2 * kHalf + kJoin + 256;   // two CTAs per SM fit
+    static constexpr int kPerSm = WR == 1 ? 2 : 1;           // CTAs
+    static constexpr int kStages = (kPerSm == 2 ? 3 : 5) * (128 / D);
+    // rows of queries, and of probabilities, lie 16 bytes further apart than
+    // they are long: ldmatrix then meets no bank twice
+    static constexpr int kQRow = 2 * D + 16, kQ = kRows * kQRow;
+    static constexpr int kPRow = 2 * kTile + 16, kP = WT > 1 ? 2 * kRows * kPRow : 0;    // for two tiles in turn
+    static constexpr int kTop = WT > 1 ? 2 * kConsumers / 2 : 0;                         // floats: row maxima, in turn
+    static constexpr int kStats = (kConsumers + kRows) * 8;  // of the join (and the fronts, before there is a tile)
+    static constexpr int kSmem = kStages * 2 * kHalf + kQ + kP + kTop * 4 + kStats + 512;
+    static_assert(kPerSm == 1 || kSmem <= 113 * 1024);
+    static_assert(kSmem <= 227 * 1024);
     static constexpr int kSlotRow = D + 4;                   // a row of a partial result: D sums, maximum, sum
     static constexpr int kSlot = kRows * kSlotRow;
 };
@@ -163,15 +199,15 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int of, int& flag, in
 }
 
 // Parts of a group, joined by the consumers of one CTA in the order of the
-// parts: written out (LAST), or to the first part's slot.  First every row's
+// parts: written out (last), or to the first part's slot.  First every row's
 // maximum and sum, several threads a row; then the weighted sums, a float4 of
 // kAcc rows a thread, kDeep parts in flight (the parts lie in the L2; their
 // latency is the cost).
-template <typename S, int D, bool LAST, typename SlotOf>
+template <typename S, int D, typename SlotOf>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, int b, int h, float* slots, int parts,
-                                           SlotOf slot_of, float* smem, int tid)
+                                           SlotOf slot_of, bool last, float* smem, int tid)
 {
-    constexpr int kSides = S::kConsumers / S::kRows;
+    constexpr int kSides = S::kConsumers / S::kRows;         // 2, 4 or 8: kConsumers is 2 kRows at least
     float2* side = reinterpret_cast<float2*>(smem);
     float2* row_stat = side + S::kConsumers;                 // maximum, 1 / sum
     auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
@@ -198,7 +234,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
             m = now;
         }
         row_stat[tid] = make_float2(m == kNegInf ? 0.f : m, 1.f);
-        if constexpr (LAST) {
+        if (last) {
             const int rr = en.row0 + tid, tok = rr / a.group;
             const bool none = en.len - en.count + tok < 0;   // a row that sees no token: zeros
             row_stat[tid].y = none ? 0.f : 1.f / l;
@@ -250,7 +286,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
 #pragma unroll
         for (int i = 0; i < kAcc; ++i) {
             const int r = r0 + i * kStep;
-            if constexpr (LAST) {
+            if (last) {
                 if (r >= en.rows) break;
                 const int rr = en.row0 + r, tok = rr / a.group;
                 const float inv = row_stat[r].y;
@@ -262,27 +298,34 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
         }
     }
     named_bar(1, S::kConsumers);
-    if constexpr (!LAST)                                     // after every thread has read the first part's maxima
+    if (!last)                                               // after every thread has read the first part's maxima
         if (tid < S::kRows) __stcg(reinterpret_cast<float2*>(part_of(0) + tid * S::kSlotRow + D), side[tid]);
 }
 
 template <int D, int WR, int WT>
-__global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
+__global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, (AttnShape<D, WR, WT>::kPerSm))
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan pl,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     using S = AttnShape<D, WR, WT>;
-    constexpr int TPW = kTile / WT;                          // tokens a warp takes of a tile
+    constexpr int TPW = kTile / WT;                          // tokens whose scores a warp takes
     constexpr int NS = TPW / 8;                              // n-tiles of its scores
-    constexpr int ND = D / 8;                                // n-tiles of its output
+    constexpr int CPW = D / WT;                              // columns of the result a warp takes
+    constexpr int ND = CPW / 8;                              // n-tiles of its result
     extern __shared__ __align__(1024) unsigned char smem[];          // the swizzle counts rows from 1024-byte borders
-    float* join = reinterpret_cast<float*>(smem + S::kStages * 2 * S::kHalf);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * 2 * S::kHalf + S::kJoin);
+    unsigned char* q_smem = smem + S::kStages * 2 * S::kHalf;
+    unsigned char* p_smem = q_smem + S::kQ;
+    float* top_smem = reinterpret_cast<float*>(p_smem + S::kP);
+    float* stats = top_smem + S::kTop;
+    uint64_t* full = reinterpret_cast<uint64_t*>(stats + S::kStats / 4);
     uint64_t* empty = full + S::kStages;
-    long long* scan = reinterpret_cast<long long*>(empty + S::kStages);
-    long long& first_base = scan[S::kThreads / 32];
-    int& first_entry = reinterpret_cast<int*>(&first_base + 1)[0];
-    int& last_flag = reinterpret_cast<int*>(&first_base + 1)[1];
+    uint64_t* told = empty + S::kStages;                     // two stretches in turn, and when they are read
+    uint64_t* heard = told + 2;
+    uint64_t* q_full = heard + 2;
+    uint64_t* q_empty = q_full + 1;
+    Stretch* notes = reinterpret_cast<Stretch*>(q_empty + 1);
+    int* flags = reinterpret_cast<int*>(notes + 2);          // last to arrive; a wait of the consumers has run out
+    static_assert((2 * S::kStages + 6) * 8 + 2 * sizeof(Stretch) + 8 <= 512);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -294,63 +337,93 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
             mbar_init(full + i, 1);
             mbar_init(empty + i, WR * WT);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(told + i, 1);
+            mbar_init(heard + i, WR * WT);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, WR * WT);
         fence_mbar_init();
+        flags[1] = 0;
     }
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---- the cut: this CTA's range [u0, u1) of all tiles ----
+    // ---- the tiles in front of every thread's entries, and all of them ----
     const int heads = a.c.n_heads;
     const int per = (pl.entries + S::kThreads - 1) / S::kThreads;
-    const int e_lo = min(pl.entries, tid * per), e_hi = min(pl.entries, e_lo + per);
-    long long mine = 0;
-    for (int e = e_lo; e < e_hi; ++e) mine += (long long)heads * entry_of(a, pl, e, S::kRows).tiles;
-    long long incl = mine;
+    int* front = reinterpret_cast<int*>(stats);              // kThreads of them, until the consumers have a tile
+    int* sums = front + S::kThreads;
+    int incl = 0;
+    const int e_end = min(pl.entries, (tid + 1) * per);
+    for (int e = tid * per; e < e_end; ++e) incl += heads * entry_of(a, pl, e, S::kRows).tiles;
+    const int mine = incl;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    long long before = incl - mine, total = 0;
+    int before = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < S::kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
+        if (w < warp) before += sums[w];
+        total += sums[w];
     }
-    if (total == 0) return;
-    const long long ctas = min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles), cta = blockIdx.x;
-    if (cta >= ctas) return;
-    const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-    if (u0 >= before && u0 < before + mine) {
-        long long base = before;
-        for (int e = e_lo; e < e_hi; ++e) {
-            const long long k = (long long)heads * entry_of(a, pl, e, S::kRows).tiles;
-            if (u0 < base + k) {
-                first_entry = e;
-                first_base = base;
-                break;
-            }
-            base += k;
-        }
-    }
+    front[tid] = before;
     __syncthreads();
+    if (total == 0) return;
+    const AttnCut cut(total, gridDim.x);
+    if ((int)blockIdx.x >= cut.ranges) return;
 
     bool alive = true;                                       // no wait has run out so far
-    int stage = 0;
-    uint32_t phase = 0;
-    int e = first_entry;
-    long long base = first_base;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!alive) return;
+        alive = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+        if (!alive && lane == 0) atomicOr(status, kStatusTimeout);
+    };
+    int stage = 0, note = 0;
+    uint32_t phase = 0, note_phase = 0, q_phase = 0;
 
     if (warp == WR * WT) {
         // ---------------------------------------------------- producer ---
+        int u = cut.first(blockIdx.x);
+        const int u1 = cut.first(blockIdx.x + 1);
+        // the entry that tile u belongs to: of the last thread whose entries begin at or in front of it
+        int behind = -1;
+#pragma unroll
+        for (int i = 0; i < S::kThreads / 32; ++i) behind += __popc(__ballot_sync(0xffffffffu, front[32 * i + lane] <= u));
+        int base = front[behind], e = behind * per;
+        Entry en = entry_of(a, pl, e, S::kRows);
         const int ps = 1 << pl.page_shift, parts = ps >= kTile ? 1 : kTile / ps, part_rows = ps < kTile ? ps : kTile;
-        for (long long u = u0; u < u1;) {
-            const Entry en = entry_of(a, pl, e, S::kRows);
-            if (en.tiles == 0) { ++e; continue; }
-            const int h = (int)((u - base) / en.tiles), off = (int)((u - base) % en.tiles);
-            const int n = (int)min((long long)(en.tiles - off), u1 - u);
+        for (bool first = true; u < u1; first = false) {
+            while (u >= base + heads * en.tiles) {
+                base += heads * en.tiles;
+                en = entry_of(a, pl, ++e, S::kRows);
+            }
+            const int h = (u - base) / en.tiles, off = (u - base) - h * en.tiles;
+            const int n = min(en.tiles - off, u1 - u), b = e / pl.row_tiles;
+            wait(heard + note, note_phase ^ 1);
+            if (lane == 0) {
+                notes[note] = Stretch{en, b, h, n, off, u - off, first};
+                mbar_arrive(told + note);
+            }
+            __syncwarp();
+            note ^= 1;
+            note_phase ^= note == 0;
+            // queries, row by row
+            wait(q_empty, q_phase ^ 1);
+            q_phase ^= 1;
+            if (alive) {
+                if (lane == 0) mbar_arrive_expect_tx(q_full, en.rows * 2 * D);
+                __syncwarp();
+                for (int r = lane; r < en.rows; r += 32) {
+                    const int rr = en.row0 + r, tok = rr / a.group;
+                    bulk_g2s(q_smem + r * S::kQRow, a.q + b * a.q_bs + tok * a.q_rs + (long long)(h * a.group + rr - tok * a.group) * D,
+                             2 * D, q_full);
+                }
+            }
             const int* row = a.c.table + (long long)en.seq * a.c.max_pages;
             const int held = (en.len + ps - 1) >> pl.page_shift;
             for (int i0 = 0; i0 < n; i0 += 32 / parts) {
@@ -370,11 +443,7 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
                 }
                 const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
                 for (int k = 0; k < 32 / parts && i0 + k < n; ++k) {
-                    if (alive) {
-                        alive = mbar_wait_bounded(empty + stage, phase ^ 1);
-                        alive = __all_sync(0xffffffffu, alive);
-                        if (!alive && lane == 0) atomicOr(status, kStatusTimeout);
-                    }
+                    wait(empty + stage, phase ^ 1);
                     if (!alive) continue;                    // no more copies; the consumers give up as well
                     const uint32_t mask = (good >> (k * parts)) & ((1u << parts) - 1);
                     unsigned char* kt = smem + stage * 2 * S::kHalf;
@@ -394,7 +463,11 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
                 }
             }
             u += n;
-            if (u == base + (long long)heads * en.tiles) { base = u; ++e; }
+        }
+        wait(heard + note, note_phase ^ 1);
+        if (lane == 0) {
+            notes[note].n = 0;
+            mbar_arrive(told + note);
         }
         return;
     }
@@ -402,34 +475,40 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
     // ------------------------------------------------------- consumers ---
     const int wr = warp / WT, wt = warp % WT;
     const int g = lane >> 2, t = lane & 3;
-    // lane's row address inside an ldmatrix group: keys 16 tokens x 16 columns, values the same transposed
+    // lane's row address inside an ldmatrix group: rows x 16 columns, values the same transposed
     const int lm_row = (lane & 7) + ((lane >> 3) & 1) * 8, lm_col = lane >> 4;
-    bool first_segment = true;
-    for (long long u = u0; u < u1;) {
-        const Entry en = entry_of(a, pl, e, S::kRows);
-        if (en.tiles == 0) { ++e; continue; }
-        const int h = (int)((u - base) / en.tiles), off = (int)((u - base) % en.tiles);
-        const int n = (int)min((long long)(en.tiles - off), u1 - u);
-        const int b = e / pl.row_tiles;
+    const auto everyone = [] { named_bar(1, S::kConsumers); };
+    const auto row_mates = [&] { named_bar(2 + wr, 32 * WT); };      // the warps that share a row tile
+    float* slots = reinterpret_cast<float*>(a.ws + ws_data_off());
+    uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off());
+    while (true) {
+        wait(told + note, note_phase);
+        if (!alive && lane == 0) flags[1] = 1;
+        everyone();
+        if (flags[1]) return;                                // all of them: none waits for another at a barrier
+        const Stretch st = notes[note];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(heard + note);
+        note ^= 1;
+        note_phase ^= note == 0;
+        if (st.n == 0) return;
+        const Entry& en = st.en;
 
-        // this lane's two rows
+        uint32_t qf[D / 16][4];
+        wait(q_full, q_phase);
+        q_phase ^= 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], smem_u32(q_smem) + (wr * 16 + lm_row) * S::kQRow + 32 * k + 16 * lm_col);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty);
+
+        // this lane's two rows; rows behind the last hold anything and are not written
         int pos[2];
-        const uint16_t* qrow[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = wr * 16 + g + 8 * i;
-            const bool ok = r < en.rows;
-            const int rr = en.row0 + (ok ? r : 0), tok = rr / a.group;
-            pos[i] = ok ? en.len - en.count + tok : -1;
-            qrow[i] = ok ? a.q + b * a.q_bs + tok * a.q_rs + (long long)(h * a.group + rr % a.group) * D : nullptr;
+            pos[i] = r < en.rows ? en.len - en.count + (en.row0 + r) / a.group : -1;
         }
-        uint32_t qf[D / 16][4];
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                qf[k][i] = qrow[i & 1] ? *reinterpret_cast<const uint32_t*>(qrow[i & 1] + 16 * k + 2 * t + 8 * (i >> 1)) : 0u;
-
         float o[ND][4], mx[2] = {kNegInf, kNegInf}, sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -440,17 +519,12 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
         const int p_first = en.len - en.count + en.row0 / a.group;
         const int p_last = en.len - en.count + (en.row0 + en.rows - 1) / a.group;
         const int all_hi = p_first + 1, all_lo = a.window ? p_last - a.window + 1 : 0;
-
         auto sees = [&](int p, int tk) { return tk <= p && (!a.window || tk > p - a.window || tk < a.sinks); };
         auto any_sees = [&](int tk) { return tk <= p_last && (!a.window || tk > p_first - a.window || tk < a.sinks); };
 
-        for (int it = 0; it < n; ++it) {
-            const int tok0 = tile_at(en, off + it) * kTile;
-            if (alive) {
-                alive = mbar_wait_bounded(full + stage, phase);
-                alive = __all_sync(0xffffffffu, alive);
-                if (!alive && lane == 0) atomicOr(status, kStatusTimeout);
-            }
+        for (int it = 0; it < st.n; ++it) {
+            const int tok0 = tile_at(en, st.off + it) * kTile;
+            wait(full + stage, phase);
             const uint32_t kt = smem_u32(smem + stage * 2 * S::kHalf), vt = kt + S::kHalf;
 
             // scores
@@ -472,14 +546,27 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
                 }
             }
             const bool whole = tok0 + kTile <= all_hi && (tok0 >= all_lo || tok0 + kTile <= a.sinks);
+            bool odd_values = false;
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tk = tok0 + wt * TPW + j * 8 + 2 * t + (i & 1), p = pos[i >> 1];
-                        s[j][i] = sees(p, tk) ? s[j][i] * pl.scale_log2 : kNegInf;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        s[j][i] = sees(pos[i >> 1], tok0 + wt * TPW + j * 8 + 2 * t + (i & 1)) ? s[j][i] * pl.scale_log2 : kNegInf;
+                // this warp's columns: what no row of the tile sees is cleared; is there anything that is not finite?
+                bool odd = false;
+#pragma unroll 1
+                for (int i = lane; i < kTile * ND; i += 32) {
+                    const int row = i / ND, chunk = wt * ND + i % ND;
+                    const uint32_t at = vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+                    if (!any_sees(tok0 + row)) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                    else odd |= (finite_halves(v[0]) & finite_halves(v[1]) & finite_halves(v[2]) & finite_halves(v[3])) != 0xffffffffu;
+                }
+                fence_proxy_async_smem();                    // before the next copy to this stage
+                odd_values = __any_sync(0xffffffffu, odd);
+                __syncwarp();                                // the cleared values are there for every lane
             } else {
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
@@ -492,14 +579,29 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
             for (int j = 0; j < NS; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[j][i]);
-            float cut[2], fix[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+            }
+            if constexpr (WT > 1) {
+                float* tops = top_smem + (it & 1) * (S::kTop / 2) + wr * (16 * WT);
+                if (t == 0) {
+                    tops[wt * 16 + g] = top[0];
+                    tops[wt * 16 + g + 8] = top[1];
+                }
+                row_mates();
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int w = 0; w < WT; ++w) top[i] = fmaxf(top[i], tops[w * 16 + g + 8 * i]);
+            }
+            float cut_at[2], fix[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 const float now = fmaxf(mx[i], top[i]);
-                cut[i] = now == kNegInf ? 0.f : now;
-                fix[i] = ex2(mx[i] - cut[i]);
+                cut_at[i] = now == kNegInf ? 0.f : now;
+                fix[i] = ex2(mx[i] - cut_at[i]);
                 mx[i] = now;
                 sum[i] *= fix[i];
             }
@@ -513,80 +615,79 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
             for (int j = 0; j < NS; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    s[j][i] = ex2(s[j][i] - cut[i >> 1] + kUp);
+                    s[j][i] = ex2(s[j][i] - cut_at[i >> 1] + kUp);
                     sum[i >> 1] += s[j][i];
                 }
-            // values
-            if (whole) {
+            // the probabilities as the operand of all 64 tokens
+            uint32_t pa[kTile / 16][4];
+            const uint32_t p_at = smem_u32(p_smem) + (it & 1) * (S::kP / 2) + wr * (16 * S::kPRow);
+            if constexpr (WT > 1) {
 #pragma unroll
-                for (int j = 0; j < NS; j += 2) {
-                    const uint32_t pa[4] = {pack2(s[j][0], s[j][1]), pack2(s[j][2], s[j][3]), pack2(s[j + 1][0], s[j + 1][1]),
-                                            pack2(s[j + 1][2], s[j + 1][3])};
-                    const int row = wt * TPW + j * 8 + lm_row;
+                for (int j = 0; j < NS; ++j)
 #pragma unroll
-                    for (int d = 0; d < ND; d += 2) {
-                        const int chunk = d + lm_col;
-                        uint32_t f[4];
-                        ldsm4t(f, vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-                        mma_16816(o[d], pa, f[0], f[1]);
-                        mma_16816(o[d + 1], pa, f[2], f[3]);
-                    }
-                }
+                    for (int i = 0; i < 2; ++i)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + (g + 8 * i) * S::kPRow + 2 * (wt * TPW + j * 8 + 2 * t)),
+                                     "r"(pack2(s[j][2 * i], s[j][2 * i + 1])) : "memory");
+                row_mates();
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) ldsm4(pa[k], p_at + lm_row * S::kPRow + 32 * k + 16 * lm_col);
             } else {
-                uint32_t finite = 0xffffffffu;
 #pragma unroll
-                for (int j = 0; j < NS; j += 2) {
-                    const uint32_t pa[4] = {pack2(s[j][0], s[j][1]), pack2(s[j][2], s[j][3]), pack2(s[j + 1][0], s[j + 1][1]),
-                                            pack2(s[j + 1][2], s[j + 1][3])};
-                    const int row = wt * TPW + j * 8 + lm_row;
-                    // tokens 2t, 2t+1 (0) and 2t+8, 2t+9 (1) of the k-step, which this lane's fragments hold: does any
-                    // row of the tile see them?
-                    uint32_t keep[2];
+                for (int k = 0; k < kTile / 16; ++k)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int tk = tok0 + wt * TPW + j * 8 + 2 * t + 8 * i;
-                        keep[i] = (any_sees(tk) ? 0xffffu : 0u) | (any_sees(tk + 1) ? 0xffff0000u : 0u);
-                    }
+                    for (int i = 0; i < 4; ++i) pa[k][i] = pack2(s[2 * k + (i >> 1)][2 * (i & 1)], s[2 * k + (i >> 1)][2 * (i & 1) + 1]);
+            }
+            // values
+            auto product = [&](auto all_finite) {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) {
+                    const int row = 16 * k + lm_row;
 #pragma unroll
                     for (int d = 0; d < ND; d += 2) {
-                        const int chunk = d + lm_col;
+                        const int chunk = wt * ND + d + lm_col;
                         uint32_t f[4];
                         ldsm4t(f, vt + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+                        if constexpr (!decltype(all_finite)::value)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[i] &= keep[i & 1];
-                            const uint32_t ok = finite_halves(f[i]);
-                            finite &= ok;
-                            f[i] &= ok;
-                        }
-                        mma_16816(o[d], pa, f[0], f[1]);
-                        mma_16816(o[d + 1], pa, f[2], f[3]);
+                            for (int i = 0; i < 4; ++i) f[i] &= finite_halves(f[i]);
+                        mma_16816(o[d], pa[k], f[0], f[1]);
+                        mma_16816(o[d + 1], pa[k], f[2], f[3]);
                     }
                 }
-                if (__any_sync(0xffffffffu, finite != 0xffffffffu)) {
-                    // values that are not finite were left out: only the rows that see them get them
-                    for (int x = 0; x < TPW; ++x) {
-                        const int tk = tok0 + wt * TPW + x, row = wt * TPW + x;
-                        float p[2];
+            };
+            if (!odd_values) {
+                product(std::true_type{});
+            } else {
+                product(std::false_type{});
+                // the values left out, token by token: only the rows that see them get them
+                for (int x = 0; x < kTile; ++x) {
+                    const int tk = tok0 + x;
+                    float p[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float mine = 0.f;
+                    for (int i = 0; i < 2; ++i) {            // row g + 8 i of column x of pa
+                        uint32_t both = 0;
 #pragma unroll
-                            for (int j = 0; j < NS; ++j)
-                                if (x >> 3 == j) mine = x & 1 ? s[j][2 * i + 1] : s[j][2 * i];
-                            p[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) | ((x & 7) >> 1));
-                        }
-                        if (!any_sees(tk)) continue;
+                        for (int k = 0; k < kTile / 16; ++k)
+                            if (x >> 4 == k) both = x & 8 ? pa[k][2 + i] : pa[k][i];
+                        both = __shfl_sync(0xffffffffu, both, (lane & ~3) | ((x & 7) >> 1));
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&both));
+                        p[i] = x & 1 ? f.y : f.x;
+                    }
+                    const bool see[2] = {sees(pos[0], tk), sees(pos[1], tk)};
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) {
-                            uint32_t v;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
-                                         : "r"(vt + (d >> 3) * (kTile * 128) + row * 128 + (((d & 7) ^ (row & 7)) << 4) + 4 * t));
-                            v &= ~finite_halves(v);
-                            const float2 vv = __half22float2(*reinterpret_cast<const __half2*>(&v));
-                            if (sees(pos[0], tk)) { o[d][0] += p[0] * vv.x; o[d][1] += p[0] * vv.y; }
-                            if (sees(pos[1], tk)) { o[d][2] += p[1] * vv.x; o[d][3] += p[1] * vv.y; }
-                        }
+                    for (int d = 0; d < ND; ++d) {
+                        const int chunk = wt * ND + d;
+                        uint32_t v;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
+                                     : "r"(vt + (chunk >> 3) * (kTile * 128) + x * 128 + (((chunk & 7) ^ (x & 7)) << 4) + 4 * t));
+                        v &= ~finite_halves(v);
+                        const float2 vv = __half22float2(*reinterpret_cast<const __half2*>(&v));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (see[i]) {
+                                o[d][2 * i] += p[i] * vv.x;
+                                o[d][2 * i + 1] += p[i] * vv.y;
+                            }
                     }
                 }
             }
@@ -595,104 +696,75 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, 2)
             if (++stage == S::kStages) { stage = 0; phase ^= 1; }
         }
 
-        // the quad's sums
+        // the sums of the quad's tokens, and of the row mates'
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
         }
-        // join the warps along the tokens, the upper half into the lower one
-#pragma unroll
-        for (int half = WT / 2; half >= 1; half /= 2) {
-            float* box = join + (wr * (WT / 2) + (wt % half)) * 16 * (D + 2);
-            if (wt >= half && wt < 2 * half) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float* at = box + (g + 8 * i) * (D + 2);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        at[8 * d + 2 * t] = o[d][2 * i];
-                        at[8 * d + 2 * t + 1] = o[d][2 * i + 1];
-                    }
-                    if (t == 0) { at[D] = mx[i]; at[D + 1] = sum[i]; }
-                }
+        if constexpr (WT > 1) {
+            float* tops = top_smem + (st.n & 1) * (S::kTop / 2) + wr * (16 * WT);
+            if (t == 0) {
+                tops[wt * 16 + g] = sum[0];
+                tops[wt * 16 + g + 8] = sum[1];
             }
-            named_bar(1, S::kConsumers);
-            if (wt < half) {
+            row_mates();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float* at = box + (g + 8 * i) * (D + 2);
-                    const float m2 = at[D], now = fmaxf(mx[i], m2), c0 = now == kNegInf ? 0.f : now;
-                    const float f1 = ex2(mx[i] - c0), f2 = ex2(m2 - c0);
-                    mx[i] = now;
-                    sum[i] = sum[i] * f1 + at[D + 1] * f2;
+            for (int i = 0; i < 2; ++i) {
+                sum[i] = 0.f;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        o[d][2 * i] = o[d][2 * i] * f1 + at[8 * d + 2 * t] * f2;
-                        o[d][2 * i + 1] = o[d][2 * i + 1] * f1 + at[8 * d + 2 * t + 1] * f2;
-                    }
-                }
+                for (int w = 0; w < WT; ++w) sum[i] += tops[w * 16 + g + 8 * i];
             }
-            named_bar(1, S::kConsumers);
+            row_mates();                                     // read before the next stretch writes there
         }
 
-        const long long gstart = base + (long long)h * en.tiles;
-        if (n == en.tiles) {
-            if (wt == 0) {
+        if (st.n == en.tiles) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = wr * 16 + g + 8 * i;
-                    if (r >= en.rows) continue;
-                    const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr % a.group;
-                    const float inv = pos[i] < 0 ? 0.f : 1.f / sum[i];    // a row that sees no token: zeros
-                    uint16_t* out = a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D;
+            for (int i = 0; i < 2; ++i) {
+                const int r = wr * 16 + g + 8 * i;
+                if (r >= en.rows) continue;
+                const int rr = en.row0 + r, tok = rr / a.group, head = st.h * a.group + rr - tok * a.group;
+                const float inv = pos[i] < 0 ? 0.f : 1.f / sum[i];    // a row that sees no token: zeros
+                uint16_t* out = a.out + st.b * a.o_bs + tok * a.o_rs + (long long)head * D + wt * CPW + 2 * t;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        *reinterpret_cast<uint32_t*>(out + 8 * d + 2 * t) = pack2(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
-                    if (a.lse && t == 0)
-                        a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] =
-                            pos[i] < 0 ? kNegInf : (mx[i] + (log2f(sum[i]) - kUp)) * kLn2;
-                }
+                for (int d = 0; d < ND; ++d)
+                    *reinterpret_cast<uint32_t*>(out + 8 * d) = pack2(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
+                if (a.lse && t == 0 && wt == 0)
+                    a.lse[((long long)st.b * a.m + tok) * a.n_q_heads + head] =
+                        pos[i] < 0 ? kNegInf : (mx[i] + (log2f(sum[i]) - kUp)) * kLn2;
             }
         } else {
-            // ---- partial result to this CTA's slot; the last CTA of the group joins ----
-            float* slots = reinterpret_cast<float*>(a.ws + ws_data_off());
-            float* slot = slots + (2 * cta + (first_segment ? 0 : 1)) * S::kSlot;
-            if (wt == 0) {
+            // ---- partial result to this range's slot; the last CTA of the group joins ----
+            float* slot = slots + (long long)(2 * blockIdx.x + (st.first ? 0 : 1)) * S::kSlot;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float* at = slot + (wr * 16 + g + 8 * i) * S::kSlotRow;
+            for (int i = 0; i < 2; ++i) {
+                float* at = slot + (wr * 16 + g + 8 * i) * S::kSlotRow;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        __stcg(reinterpret_cast<float2*>(at + 8 * d + 2 * t), make_float2(o[d][2 * i], o[d][2 * i + 1]));
-                    if (t == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
-                }
+                for (int d = 0; d < ND; ++d)
+                    __stcg(reinterpret_cast<float2*>(at + wt * CPW + 8 * d + 2 * t), make_float2(o[d][2 * i], o[d][2 * i + 1]));
+                if (t == 0 && wt == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
             }
-            // the group's parts: the first one is its CTA's first or last segment, the others first segments
-            const int c_first = cta_of_unit(gstart, ctas, total), c_last = cta_of_unit(gstart + en.tiles - 1, ctas, total);
-            const int parts = c_last - c_first + 1, late = gstart == total * c_first / ctas ? 0 : 1;
-            auto slot_of = [&](int c) { return 2 * (c_first + c) + (c == 0 ? late : 0); };
-            const int mine = (int)cta - c_first;
+            // the group's parts: the first one is its range's first or last stretch, the others first ones
+            const int r_first = cut.range_of(st.gstart), parts = cut.range_of(st.gstart + en.tiles - 1) - r_first + 1;
+            const int late = st.gstart == cut.first(r_first) ? 0 : 1;
+            auto slot_of = [&](int c) { return 2 * (r_first + c) + (c == 0 ? late : 0); };
             // up to kFan parts are joined at once, more in two levels of about the square root
             int fan = parts;
             if (parts > kFan)
                 for (fan = kFan / 2; fan * fan < parts; ++fan) {}
-            uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off());
-            const int node = mine / fan * fan, in_node = min(fan, parts - node);
-            if (last_of(counters + slot_of(node), in_node, last_flag, tid, S::kConsumers)) {
-                if (fan == parts) {
-                    join_parts<S, D, true>(a, en, b, h, slots, parts, slot_of, join, tid);
-                } else {
-                    join_parts<S, D, false>(a, en, b, h, slots, in_node, [&](int c) { return slot_of(node + c); }, join, tid);
-                    const int nodes = (parts + fan - 1) / fan;
-                    if (last_of(counters + 2 * kMaxCtas + slot_of(0), nodes, last_flag, tid, S::kConsumers))
-                        join_parts<S, D, true>(a, en, b, h, slots, nodes, [&](int c) { return slot_of(c * fan); }, join, tid);
-                }
+            const int node = ((int)blockIdx.x - r_first) / fan * fan;
+            int from = node, step = 1, count = min(fan, parts - node);
+            uint32_t* counter = counters + slot_of(node);
+            while (last_of(counter, count, flags[0], tid, S::kConsumers)) {
+                const bool last = step == fan || fan == parts;
+                join_parts<S, D>(a, en, st.b, st.h, slots, count, [&](int c) { return slot_of(from + c * step); }, last, stats, tid);
+                if (last) break;
+                from = 0;
+                step = fan;
+                count = (parts + fan - 1) / fan;
+                counter = counters + 2 * kMaxCtas + slot_of(0);
             }
         }
-        first_segment = false;
-        u += n;
-        if (u == base + (long long)heads * en.tiles) { base = u; ++e; }
     }
 }
 
@@ -732,15 +804,25 @@ cudaError_t layer_map(CUtensorMap& map, EncodeFn fn, const KvArgs& c, uint16_t* 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows per tile: the smallest that holds a (sequence, head)'s rows, up to 64.
-int attn_tile_rows(int m, int group)
+// The rows (new tokens x query heads) of a head of the cache are cut into equal
+// tiles of up to 128 rows, in 16s; with 64 rows or fewer several warps share 16.
+struct AttnRows {
+    int row_tiles, warps_r, ctas;
+};
+
+AttnRows attn_rows(int m, int group)
 {
+    AttnRows r;
     const int rows = m * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    r.row_tiles = (rows + 127) / 128;
+    r.warps_r = ((rows + r.row_tiles - 1) / r.row_tiles + 15) / 16;
+    r.ctas = r.warps_r == 1 ? kMaxCtas : kMaxCtas / 2;
+    return r;
 }
+static_assert(4 * kMaxCtas <= kMaxBlocks);                   // two counters a slot
 
 template <int D, int WR, int WT>
-cudaError_t launch_attn_t(const AttnArgs& a, cudaStream_t stream)
+cudaError_t launch_attn_t(const AttnArgs& a, const AttnRows& rows, cudaStream_t stream)
 {
     using S = AttnShape<D, WR, WT>;
     auto kern = paged_attn_kernel<D, WR, WT>;
@@ -755,29 +837,47 @@ cudaError_t launch_attn_t(const AttnArgs& a, cudaStream_t stream)
     if ((e = layer_map(kmap, fn, a.c, a.c.k, a.layer)) != cudaSuccess) return e;
     if ((e = layer_map(vmap, fn, a.c, a.c.v, a.layer)) != cudaSuccess) return e;
     AttnPlan pl;
-    pl.row_tiles = (a.m * a.group + S::kRows - 1) / S::kRows;
+    pl.row_tiles = rows.row_tiles;
     pl.entries = a.n * pl.row_tiles;
     pl.page_shift = __builtin_ctz(a.c.page_size);
     pl.scale_log2 = a.scale * 1.4426950408889634f;
-    return launch_pdl(kern, dim3(kMaxCtas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+    return launch_pdl(kern, dim3((unsigned)rows.ctas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+}
+
+template <int D>
+cudaError_t launch_attn_d(const AttnArgs& a, const AttnRows& rows, cudaStream_t stream)
+{
+    switch (rows.warps_r) {
+        case 1: return launch_attn_t<D, 1, 4>(a, rows, stream);
+        case 2: return launch_attn_t<D, 2, 4>(a, rows, stream);
+        case 3: return launch_attn_t<D, 3, 2>(a, rows, stream);
+        case 4: return launch_attn_t<D, 4, 2>(a, rows, stream);
+        case 5: return launch_attn_t<D, 5, 1>(a, rows, stream);
+        case 6: return launch_attn_t<D, 6, 1>(a, rows, stream);
+        case 7: return launch_attn_t<D, 7, 1>(a, rows, stream);
+        default: return launch_attn_t<D, 8, 1>(a, rows, stream);
+    }
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim)
 {
-    const int rows = attn_tile_rows(m, n_q_heads / n_heads);
-    return ws_data_off() + align_up(sizeof(float) * 2 * (size_t)kMaxCtas * rows * (head_dim + 4), 256);
+    const AttnRows r = attn_rows(m, n_q_heads / n_heads);
+    return ws_data_off() + align_up(sizeof(float) * 2 * (size_t)r.ctas * 16 * r.warps_r * (head_dim + 4), 256);
+}
+
+bool attention_tiles_ok(const AttnArgs& a)
+{
+    const AttnRows r = attn_rows(a.m, a.group);
+    const long long tokens = (long long)a.c.max_pages * a.c.page_size;
+    return (long long)a.n * r.row_tiles * a.c.n_heads * (tokens / kTile + 2) < (1ll << 31) - (1 << 20);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream)
 {
-    const int rows = attn_tile_rows(a.m, a.group);
-    if (a.c.head_dim == 128)
-        return rows == 16 ? launch_attn_t<128, 1, 4>(a, stream)
-                          : rows == 32 ? launch_attn_t<128, 2, 2>(a, stream) : launch_attn_t<128, 4, 1>(a, stream);
-    return rows == 16 ? launch_attn_t<64, 1, 4>(a, stream)
-                      : rows == 32 ? launch_attn_t<64, 2, 2>(a, stream) : launch_attn_t<64, 4, 1>(a, stream);
+    const AttnRows rows = attn_rows(a.m, a.group);
+    return a.c.head_dim == 128 ? launch_attn_d<128>(a, rows, stream) : launch_attn_d<64>(a, rows, stream);
 }
 
 }  // namespace exl3

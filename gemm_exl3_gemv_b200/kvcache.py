@@ -183,11 +183,11 @@ class KvCache:
         sequence (any number n of sequences)."""
         if n < 0:
             raise ValueError("n: expected a number of sequences")
-        need = max(int(ex.lib.exl3_paged_attention_workspace_bytes(r, n_q_heads, self.n_heads, self.head_dim))
-                   for r in (m, 1))
-        if need == 0 or m < 1:
+        need = [int(ex.lib.exl3_paged_attention_workspace_bytes(r, n_q_heads, self.n_heads, self.head_dim))
+                for r in range(1, m + 1)]
+        if not all(need) or not need:
             raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"attention of {m} rows with {n_q_heads} heads")
-        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return torch.zeros(max(need), dtype=torch.uint8, device=self.device)
 
     def attention(self, layer: int, seqs: torch.Tensor, q: torch.Tensor, counts: Optional[torch.Tensor] = None,
                   scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,

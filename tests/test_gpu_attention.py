@@ -280,26 +280,30 @@ def test_graph_follows_the_lengths(ex):
 
 
 def test_bad_numbers_are_not_followed(ex):
-    """Sequence numbers and table entries out of range: reported, not read; rows of good sequences are right."""
-    import torch
+    """Sequence numbers and table entries out of range: reported, not read; rows of good sequences are right
+    (to rounding: where a sequence's sums are cut depends on the whole batch)."""
     c = Case([70, 90, 40], [1, 1, 1], dim=64, page=16, seed=16)
-    want = c.run()[0].clone()
     good = c.cache.table.clone()
+    seqs, counts = list(c.seqs), list(c.counts)
+
+    def check(got, rows):
+        assert c.cache.status() == ex.EXL3_ERR_INDEX
+        for r in rows:
+            c.seqs, c.counts, q = [seqs[r]], [1], c.q
+            c.q = q[r:r + 1]
+            c.check([x[r:r + 1] for x in got])
+            c.seqs, c.counts, c.q = list(seqs), list(counts), q
+
     c.seqs = [0, 3, 2]
-    got = c.run()[0]
-    assert c.cache.status() == ex.EXL3_ERR_INDEX
-    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and (got[1] == 77).all()
-    c.seqs = [0, 1, 2]
+    got = c.run()
+    assert (got[0][1] == 77).all() and (got[1][1] == 77).all()
+    check(got, [0, 2])
     for bad in (-5, c.cache.n_pages, 2 ** 31 - 1):
         c.cache.table[1, 2] = bad
-        got = c.run()[0]
-        assert c.cache.status() == ex.EXL3_ERR_INDEX
-        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+        check(c.run(), [0, 2])
         c.cache.table.copy_(good)
     c.cache.lens[0] = 2 ** 30                                # far past the table: taken as a full row of it
-    got = c.run()[0]
-    assert c.cache.status() == ex.EXL3_ERR_INDEX
-    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    check(c.run(), [1, 2])
 
 
 def test_refusals(ex):
