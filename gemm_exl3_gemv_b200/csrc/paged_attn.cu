@@ -49,7 +49,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // o): the largest is 2^14, and what is 2^-28 of it is still a normal number.
 constexpr float kUp = 14.f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinTiles = 4;                                 // of a CTA's share, from which another CTA is worth its part of the join
+constexpr int kMinTiles = 2;                                 // of a CTA's share, from which another CTA is worth its part of the join
 constexpr int kFan = 8;                                      // parts joined at once
 constexpr int kMaxCtas = 148 * 2;
 
@@ -168,98 +168,60 @@ struct AttnShape {
     static constexpr int kRows = 16 * WR;
     static constexpr int kHalf = kTile * D * 2;              // bytes of a tile's keys (or values)
     static constexpr int kPerSm = WR == 1 ? 2 : 1;           // CTAs
-    static constexpr int kStages = (kPerSm == 2 ? 3 : 5) * (128 / D);
     // rows of queries, and of probabilities, lie 16 bytes further apart than
     // they are long: ldmatrix then meets no bank twice
     static constexpr int kQRow = 2 * D + 16, kQ = kRows * kQRow;
     static constexpr int kPRow = 2 * kTile + 16, kP = WT > 1 ? 2 * kRows * kPRow : 0;    // for two tiles in turn
     static constexpr int kTop = WT > 1 ? 2 * kConsumers / 2 : 0;                         // floats: row maxima, in turn
-    static constexpr int kStats = (kConsumers + kRows) * 8;  // of the join (and the fronts, before there is a tile)
-    static constexpr int kSmem = kStages * 2 * kHalf + kQ + kP + kTop * 4 + kStats + 512;
-    static_assert(kPerSm == 1 || kSmem <= 113 * 1024);
-    static_assert(kSmem <= 227 * 1024);
+    static constexpr int kFronts = (kThreads + kThreads / 32 + 3) / 4 * 16;              // until the producer has read them
+    static constexpr int kRest = kQ + kP + kTop * 4 + kFronts + 512, kRoom = (kPerSm == 2 ? 113 : 227) * 1024 - kRest;
+    static constexpr int kStages = kRoom / (2 * kHalf) < 8 ? kRoom / (2 * kHalf) : 8;    // of the ring: as many as fit
+    static constexpr int kSmem = kStages * 2 * kHalf + kRest;
     static constexpr int kSlotRow = D + 4;                   // a row of a partial result: D sums, maximum, sum
     static constexpr int kSlot = kRows * kSlotRow;
 };
 
 // Counts the calling CTA in; true in the last of `of` CTAs, which may then read
-// what the others wrote before they were counted.  Consumer threads.
+// what the others wrote before they were counted.  Consumer threads: the
+// barriers order the other threads' accesses around the first one's fences.
 __device__ __forceinline__ bool last_of(uint32_t* counter, int of, int& flag, int tid, int threads)
 {
-    __threadfence();
     named_bar(1, threads);
     if (tid == 0) {
+        __threadfence();
         flag = atomicAdd(counter, 1u) == (uint32_t)of - 1;
         if (flag) *counter = 0;
+        __threadfence();
     }
     named_bar(1, threads);
-    const bool last = flag;
-    if (last) __threadfence();
-    return last;
+    return flag;
 }
 
 // Parts of a group, joined by the consumers of one CTA in the order of the
-// parts: written out (last), or to the first part's slot.  First every row's
-// maximum and sum, several threads a row; then the weighted sums, a float4 of
-// kAcc rows a thread, kDeep parts in flight (the parts lie in the L2; their
-// latency is the cost).
+// parts: written out (last), or to the first part's slot.  A thread takes a
+// float4 of kAcc rows, with kDeep parts in flight (the parts lie in the L2;
+// their latency is the cost), and rescales by the rows' maxima as it goes.
 template <typename S, int D, typename SlotOf>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, int b, int h, float* slots, int parts,
-                                           SlotOf slot_of, bool last, float* smem, int tid)
+                                           SlotOf slot_of, bool last, int tid)
 {
-    constexpr int kSides = S::kConsumers / S::kRows;         // 2, 4 or 8: kConsumers is 2 kRows at least
-    float2* side = reinterpret_cast<float2*>(smem);
-    float2* row_stat = side + S::kConsumers;                 // maximum, 1 / sum
-    auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
-    {
-        const int r = tid % S::kRows, first = tid / S::kRows;
-        float m = kNegInf, l = 0.f;
-#pragma unroll 4
-        for (int c = first; c < parts; c += kSides) {
-            const float2 ms = __ldcg(reinterpret_cast<const float2*>(part_of(c) + r * S::kSlotRow + D));
-            const float now = fmaxf(m, ms.x), c0 = now == kNegInf ? 0.f : now;
-            l = l * ex2(m - c0) + ms.y * ex2(ms.x - c0);
-            m = now;
-        }
-        side[tid] = make_float2(m, l);
-    }
-    named_bar(1, S::kConsumers);
-    if (tid < S::kRows) {
-        float m = kNegInf, l = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSides; ++i) {
-            const float2 ms = side[i * S::kRows + tid];
-            const float now = fmaxf(m, ms.x), c0 = now == kNegInf ? 0.f : now;
-            l = l * ex2(m - c0) + ms.y * ex2(ms.x - c0);
-            m = now;
-        }
-        row_stat[tid] = make_float2(m == kNegInf ? 0.f : m, 1.f);
-        if (last) {
-            const int rr = en.row0 + tid, tok = rr / a.group;
-            const bool none = en.len - en.count + tok < 0;   // a row that sees no token: zeros
-            row_stat[tid].y = none ? 0.f : 1.f / l;
-            if (a.lse && tid < en.rows)
-                a.lse[((long long)b * a.m + tok) * a.n_q_heads + h * a.group + rr % a.group] =
-                    none ? kNegInf : (m + (log2f(l) - kUp)) * kLn2;
-        } else {
-            side[tid] = make_float2(m, l);                   // this thread alone reads and writes it from here on
-        }
-    }
-    named_bar(1, S::kConsumers);
     constexpr int kVec = D / 4, kStep = S::kConsumers / kVec;    // rows apart
     constexpr int kAcc = S::kRows / kStep < 4 ? S::kRows / kStep : 4, kDeep = 4;
+    static_assert(S::kRows % (kStep * kAcc) == 0);
+    auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
     const int col = 4 * (tid % kVec);
     for (int r0 = tid / kVec; r0 < S::kRows; r0 += kStep * kAcc) {
         float4 acc[kAcc];
-        float top[kAcc];
+        float mx[kAcc], sum[kAcc];
 #pragma unroll
         for (int i = 0; i < kAcc; ++i) {
             acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            top[i] = row_stat[r0 + i * kStep].x;
+            mx[i] = kNegInf;
+            sum[i] = 0.f;
         }
         for (int c0 = 0; c0 < parts; c0 += kDeep) {
             float4 v[kDeep][kAcc];
-            float w[kDeep][kAcc];
+            float2 ms[kDeep][kAcc];
 #pragma unroll
             for (int c = 0; c < kDeep; ++c) {
                 const float* from = part_of(min(c0 + c, parts - 1));
@@ -267,15 +229,23 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
                 for (int i = 0; i < kAcc; ++i) {
                     const float* at = from + (r0 + i * kStep) * S::kSlotRow;
                     v[c][i] = __ldcg(reinterpret_cast<const float4*>(at + col));
-                    w[c][i] = __ldcg(at + D);
+                    ms[c][i] = __ldcg(reinterpret_cast<const float2*>(at + D));
                 }
             }
 #pragma unroll
-            for (int c = 0; c < kDeep; ++c) {
-                if (c0 + c >= parts) break;
+            for (int i = 0; i < kAcc; ++i) {
+                float now = mx[i];
 #pragma unroll
-                for (int i = 0; i < kAcc; ++i) {
-                    const float f = ex2(w[c][i] - top[i]);
+                for (int c = 0; c < kDeep; ++c) now = fmaxf(now, ms[c][i].x);    // the last part again does not matter
+                const float at = now == kNegInf ? 0.f : now, f0 = ex2(mx[i] - at);
+                mx[i] = now;
+                sum[i] *= f0;
+                acc[i].x *= f0, acc[i].y *= f0, acc[i].z *= f0, acc[i].w *= f0;
+#pragma unroll
+                for (int c = 0; c < kDeep; ++c) {
+                    if (c0 + c >= parts) break;
+                    const float f = ex2(ms[c][i].x - at);
+                    sum[i] += f * ms[c][i].y;
                     acc[i].x += f * v[c][i].x;
                     acc[i].y += f * v[c][i].y;
                     acc[i].z += f * v[c][i].z;
@@ -283,23 +253,27 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
                 }
             }
         }
+        // row maxima of the first part are read by other threads until here
+        if (!last) named_bar(1, S::kConsumers);
 #pragma unroll
         for (int i = 0; i < kAcc; ++i) {
             const int r = r0 + i * kStep;
             if (last) {
                 if (r >= en.rows) break;
-                const int rr = en.row0 + r, tok = rr / a.group;
-                const float inv = row_stat[r].y;
-                *reinterpret_cast<uint2*>(a.out + b * a.o_bs + tok * a.o_rs + (long long)(h * a.group + rr % a.group) * D + col) =
+                const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr - tok * a.group;
+                const bool none = en.len - en.count + tok < 0;    // a row that sees no token: zeros
+                const float inv = none ? 0.f : 1.f / sum[i];
+                *reinterpret_cast<uint2*>(a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D + col) =
                     make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
+                if (a.lse && col == 0)
+                    a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] = none ? kNegInf : (mx[i] + (log2f(sum[i]) - kUp)) * kLn2;
             } else {
-                __stcg(reinterpret_cast<float4*>(part_of(0) + r * S::kSlotRow + col), acc[i]);
+                float* at = part_of(0) + r * S::kSlotRow;
+                __stcg(reinterpret_cast<float4*>(at + col), acc[i]);
+                if (col == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
             }
         }
     }
-    named_bar(1, S::kConsumers);
-    if (!last)                                               // after every thread has read the first part's maxima
-        if (tid < S::kRows) __stcg(reinterpret_cast<float2*>(part_of(0) + tid * S::kSlotRow + D), side[tid]);
 }
 
 template <int D, int WR, int WT>
@@ -316,8 +290,8 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, (AttnShape<D, 
     unsigned char* q_smem = smem + S::kStages * 2 * S::kHalf;
     unsigned char* p_smem = q_smem + S::kQ;
     float* top_smem = reinterpret_cast<float*>(p_smem + S::kP);
-    float* stats = top_smem + S::kTop;
-    uint64_t* full = reinterpret_cast<uint64_t*>(stats + S::kStats / 4);
+    int* front = reinterpret_cast<int*>(top_smem + S::kTop);
+    uint64_t* full = reinterpret_cast<uint64_t*>(front + S::kFronts / 4);
     uint64_t* empty = full + S::kStages;
     uint64_t* told = empty + S::kStages;                     // two stretches in turn, and when they are read
     uint64_t* heard = told + 2;
@@ -352,7 +326,6 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, (AttnShape<D, 
     // ---- the tiles in front of every thread's entries, and all of them ----
     const int heads = a.c.n_heads;
     const int per = (pl.entries + S::kThreads - 1) / S::kThreads;
-    int* front = reinterpret_cast<int*>(stats);              // kThreads of them, until the consumers have a tile
     int* sums = front + S::kThreads;
     int incl = 0;
     const int e_end = min(pl.entries, (tid + 1) * per);
@@ -757,7 +730,7 @@ __global__ void __launch_bounds__(AttnShape<D, WR, WT>::kThreads, (AttnShape<D, 
             uint32_t* counter = counters + slot_of(node);
             while (last_of(counter, count, flags[0], tid, S::kConsumers)) {
                 const bool last = step == fan || fan == parts;
-                join_parts<S, D>(a, en, st.b, st.h, slots, count, [&](int c) { return slot_of(from + c * step); }, last, stats, tid);
+                join_parts<S, D>(a, en, st.b, st.h, slots, count, [&](int c) { return slot_of(from + c * step); }, last, tid);
                 if (last) break;
                 from = 0;
                 step = fan;
@@ -850,11 +823,11 @@ cudaError_t launch_attn_d(const AttnArgs& a, const AttnRows& rows, cudaStream_t 
     switch (rows.warps_r) {
         case 1: return launch_attn_t<D, 1, 4>(a, rows, stream);
         case 2: return launch_attn_t<D, 2, 4>(a, rows, stream);
-        case 3: return launch_attn_t<D, 3, 2>(a, rows, stream);
+        case 3: return launch_attn_t<D, 3, 4>(a, rows, stream);
         case 4: return launch_attn_t<D, 4, 2>(a, rows, stream);
-        case 5: return launch_attn_t<D, 5, 1>(a, rows, stream);
-        case 6: return launch_attn_t<D, 6, 1>(a, rows, stream);
-        case 7: return launch_attn_t<D, 7, 1>(a, rows, stream);
+        case 5: return launch_attn_t<D, 5, 2>(a, rows, stream);
+        case 6: return launch_attn_t<D, 6, 2>(a, rows, stream);
+        case 7: return launch_attn_t<D, 7, 2>(a, rows, stream);
         default: return launch_attn_t<D, 8, 1>(a, rows, stream);
     }
 }
