@@ -224,26 +224,26 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, i
             float2 ms[kDeep][kAcc];
 #pragma unroll
             for (int c = 0; c < kDeep; ++c) {
-                const float* from = part_of(min(c0 + c, parts - 1));
+                const float* from = part_of(c0 + c);
 #pragma unroll
                 for (int i = 0; i < kAcc; ++i) {
                     const float* at = from + (r0 + i * kStep) * S::kSlotRow;
-                    v[c][i] = __ldcg(reinterpret_cast<const float4*>(at + col));
-                    ms[c][i] = __ldcg(reinterpret_cast<const float2*>(at + D));
+                    const bool in = c0 + c < parts;
+                    v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(at + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ms[c][i] = in ? __ldcg(reinterpret_cast<const float2*>(at + D)) : make_float2(kNegInf, 0.f);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kAcc; ++i) {
                 float now = mx[i];
 #pragma unroll
-                for (int c = 0; c < kDeep; ++c) now = fmaxf(now, ms[c][i].x);    // the last part again does not matter
+                for (int c = 0; c < kDeep; ++c) now = fmaxf(now, ms[c][i].x);
                 const float at = now == kNegInf ? 0.f : now, f0 = ex2(mx[i] - at);
                 mx[i] = now;
                 sum[i] *= f0;
                 acc[i].x *= f0, acc[i].y *= f0, acc[i].z *= f0, acc[i].w *= f0;
 #pragma unroll
                 for (int c = 0; c < kDeep; ++c) {
-                    if (c0 + c >= parts) break;
                     const float f = ex2(ms[c][i].x - at);
                     sum[i] += f * ms[c][i].y;
                     acc[i].x += f * v[c][i].x;
