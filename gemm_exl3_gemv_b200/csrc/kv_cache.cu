@@ -78,130 +78,171 @@ __global__ void __launch_bounds__(256) kv_reset_kernel(KvArgs a)
 }
 
 // ----------------------------------------------------------------- extend ---
-// grid (list entries, copiers).  Every CTA sums up what the whole list needs;
-// the CTAs of entry b take its pages, lowest first, from the free bits, and
-// share the copy of its last page if others hold that page too.  The table
-// entry of such a page, the lengths, the reference counts and the free bits
-// are what other CTAs still read: the last CTA to arrive writes them.
+// Every CTA works out what the whole list needs: per entry, how many pages and
+// whether its last page has to be copied first because others hold it too.
+// The lowest free pages are given out in the order of the list.  The copies,
+// in runs of one layer's and head's tokens, are shared out over the CTAs; the
+// last CTA to be done writes the bookkeeping, which the others have read.
+// Without copies the first CTA is the only one that stays.
 
 constexpr int kExtThreads = 256;
+constexpr int kExtPer = kKvMaxList / kExtThreads;            // list entries of a thread, at most
 
 __global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n, int m, const int* seqs, const int* counts)
 {
     extern __shared__ uint32_t seen[];                       // n_seqs bits
     __shared__ int tmp[33];
-    __shared__ int copy_to, is_last;
-    const int tid = threadIdx.x, b = blockIdx.x, ps = a.page_size;
-    const int seen_words = (a.n_seqs + 31) / 32;
-    for (int i = tid; i < seen_words; i += kExtThreads) seen[i] = 0;
+    __shared__ int ahead[kKvMaxList + 1];                    // pages that the entries in front take
+    __shared__ int copies[kKvMaxList];                       // entries whose last page is copied, in the list's order
+    __shared__ int found, is_last;
+    const int tid = threadIdx.x, ps = a.page_size;
+    for (int i = tid; i < (a.n_seqs + 31) / 32; i += kExtThreads) seen[i] = 0;
     grid_dep_wait();
     grid_dep_launch();
     const int old_fault = __ldcg(a.scratch + kKvFault);
     __syncthreads();
 
-    // needs of this thread's entries (a contiguous run of the list)
-    const int per = (n + kExtThreads - 1) / kExtThreads;
-    const int e0 = min(n, tid * per), e1 = min(n, e0 + per);
-    int need = 0, bad = 0, my_need = 0, my_before = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int s = seqs[e], c = counts ? counts[e] : m;
-        if (!mark(seen, s, a.n_seqs) || c < 0 || c > m) { bad |= kKvIndex; continue; }
-        const int old = a.lens[s];
-        if (old < 0 || old > a.max_pages * ps) { bad |= kKvIndex; continue; }
-        if (c > a.max_pages * ps - old) { bad |= kKvFull; continue; }
-        int k = pages_of(old + c, ps) - pages_of(old, ps);
-        if (c > 0 && old % ps) {
-            const int p = a.table[(long long)s * a.max_pages + old / ps];
+    // this thread's entries: a contiguous run of the list
+    const int per = (n + kExtThreads - 1) / kExtThreads, e0 = min(n, tid * per), e1 = min(n, e0 + per);
+    int seq[kExtPer], count[kExtPer], old[kExtPer], need[kExtPer];
+    bool copy[kExtPer];
+    int needs = 0, copied = 0, bad = 0;
+#pragma unroll
+    for (int i = 0; i < kExtPer; ++i) {
+        need[i] = 0;
+        copy[i] = false;
+        if (i >= e1 - e0) continue;
+        seq[i] = seqs[e0 + i];
+        count[i] = counts ? counts[e0 + i] : m;
+        if (!mark(seen, seq[i], a.n_seqs) || count[i] < 0 || count[i] > m) { bad |= kKvIndex; continue; }
+        old[i] = a.lens[seq[i]];
+        if (old[i] < 0 || old[i] > a.max_pages * ps) { bad |= kKvIndex; continue; }
+        if (count[i] > a.max_pages * ps - old[i]) { bad |= kKvFull; continue; }
+        need[i] = pages_of(old[i] + count[i], ps) - pages_of(old[i], ps);
+        if (count[i] > 0 && old[i] % ps) {
+            const int p = a.table[(long long)seq[i] * a.max_pages + old[i] / ps];
             if (!page_ok(a, p)) { bad |= kKvIndex; continue; }
-            k += __ldcg(a.refs + p) > 1;
+            copy[i] = __ldcg(a.refs + p) > 1;
+            need[i] += copy[i];
         }
-        if (e == b) my_before = need, my_need = k;
-        need += k;
+        needs += need[i];
+        copied += copy[i];
     }
-    int before;
-    const int total = block_scan<kExtThreads>(need, before, tmp);
-    __shared__ int entry_before, entry_need;
-    if (b >= e0 && b < e1) { entry_before = before + my_before; entry_need = my_need; }
+    int at, copy_at;
+    const int total = block_scan<kExtThreads>(needs, at, tmp);
+    const int n_copies = block_scan<kExtThreads>(copied, copy_at, tmp);
+#pragma unroll
+    for (int i = 0; i < kExtPer; ++i) {
+        if (i >= e1 - e0) continue;
+        ahead[e0 + i] = at;
+        at += need[i];
+        if (copy[i]) copies[copy_at++] = e0 + i;
+    }
+    if (tid == 0) ahead[n] = total;
     bad = __syncthreads_or(bad & kKvIndex) ? kKvIndex : __syncthreads_or(bad & kKvFull) ? kKvFull : 0;
 
     // the free bits of this thread's words, and how many lie in front
     const int words = (a.n_pages + 31) / 32, wper = (words + kExtThreads - 1) / kExtThreads;
     const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
-    int free_before = 0;
+    int free_before = 0, have = 0;
     if (!bad && total > 0) {
-        int have = 0;
         for (int w = w0; w < w1; ++w) have += __popc(__ldcg(a.free + w));
-        const int all = block_scan<kExtThreads>(have, free_before, tmp);
-        if (total > all) bad = kKvFull;
+        if (block_scan<kExtThreads>(have, free_before, tmp) < total) bad = kKvFull;
     }
     if (bad || old_fault) {
-        if (bad && b == 0 && blockIdx.y == 0 && tid == 0) fault(a, bad);
+        if (bad && blockIdx.x == 0 && tid == 0) fault(a, bad);
         return;                                              // the same answer in every CTA
     }
 
-    const int s = seqs[b], c = counts ? counts[b] : m, old = a.lens[s];
-    const int first_new = pages_of(old, ps), fresh = pages_of(old + c, ps) - first_new;
-    const bool copy = entry_need > fresh;
-    if (entry_need > 0 && (blockIdx.y == 0 || copy)) {
-        const int r0 = entry_before, r1 = entry_before + entry_need;
-        int rank = free_before;
-        for (int w = w0; w < w1 && rank < r1; ++w) {
-            uint32_t bits = __ldcg(a.free + w);
-            const int k = __popc(bits);
-            if (rank + k <= r0) { rank += k; continue; }
-            for (; bits && rank < r1; bits &= bits - 1, ++rank) {
-                if (rank < r0) continue;
-                const int page = 32 * w + __ffs(bits) - 1, nth = rank - r0;
-                if (copy && nth == 0) {
-                    copy_to = page;
-                    if (blockIdx.y == 0) a.scratch[kKvCopy + b] = page;
-                } else if (blockIdx.y == 0) {
-                    a.table[(long long)s * a.max_pages + first_new + nth - (copy ? 1 : 0)] = page;
-                }
+    // copies: item (copy, layer, head, key or value)
+    const int runs = 2 * a.n_layers * a.n_heads;
+    const long long items = (long long)n_copies * runs;
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, items));
+    if ((int)blockIdx.x >= ctas) return;
+    const long long page_vec = (long long)a.n_heads * ps * a.head_dim / 8, layer_vec = page_vec * a.n_pages;
+    int from = 0, to = 0, run = 0, last_copy = -1;
+    for (long long it = blockIdx.x; it < items; it += ctas) {
+        const int c = (int)(it / runs), r = (int)(it % runs), layer = (r >> 1) / a.n_heads, h = (r >> 1) % a.n_heads;
+        if (c != last_copy) {
+            // the page it goes to: the entry's first, of rank ahead[entry] among the free ones
+            const int e = copies[c], rank = ahead[e];
+            __syncthreads();
+            if (rank >= free_before && rank < free_before + have) {
+                int left = rank - free_before, w = w0;
+                uint32_t bits = __ldcg(a.free + w);
+                for (int k; left >= (k = __popc(bits)); left -= k) bits = __ldcg(a.free + ++w);
+                while (left-- > 0) bits &= bits - 1;
+                found = 32 * w + __ffs(bits) - 1;
             }
+            __syncthreads();
+            const int s = seqs[e], len = a.lens[s];
+            to = found;
+            from = a.table[(long long)s * a.max_pages + len / ps];
+            run = (len % ps) * a.head_dim / 8;               // 16-byte pieces
+            last_copy = c;
         }
-    }
-    if (blockIdx.y == 0 && !copy && tid == 0) a.scratch[kKvCopy + b] = -1;
-    if (copy) {
-        __syncthreads();
-        // tokens of the shared page: per layer and head one run of old % ps rows
-        const int from = a.table[(long long)s * a.max_pages + old / ps], to = copy_to;
-        const int run = (old % ps) * a.head_dim / 8;         // 16-byte pieces
-        const long long page_vec = (long long)a.n_heads * ps * a.head_dim / 8, layer_vec = page_vec * a.n_pages;
-        const int runs = a.n_layers * a.n_heads;
-        for (int i = blockIdx.y; i < 2 * runs; i += gridDim.y) {
-            const int r = i >> 1, layer = r / a.n_heads, h = r % a.n_heads;
-            uint4* base = reinterpret_cast<uint4*>(i & 1 ? a.v : a.k) + layer * layer_vec + (long long)h * ps * a.head_dim / 8;
-            for (int x = tid; x < run; x += kExtThreads) base[to * page_vec + x] = base[from * page_vec + x];
+        uint4* base = reinterpret_cast<uint4*>(r & 1 ? a.v : a.k) + layer * layer_vec + (long long)h * ps * a.head_dim / 8;
+        const uint4* src = base + from * page_vec;
+        uint4* dst = base + to * page_vec;
+        for (int x = tid; x < run; x += 4 * kExtThreads) {
+            uint4 buf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (x + i * kExtThreads < run) buf[i] = src[x + i * kExtThreads];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (x + i * kExtThreads < run) dst[x + i * kExtThreads] = buf[i];
         }
     }
 
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) is_last = atomicAdd(a.scratch + kKvArrived, 1) == (int)(gridDim.x * gridDim.y) - 1;
-    __syncthreads();
-    if (!is_last) return;
-    __threadfence();
-    if (tid == 0) a.scratch[kKvArrived] = 0;
-    // the lowest `total` free pages are taken
-    int rank = free_before;
+    if (ctas > 1) {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            is_last = atomicAdd(a.scratch + kKvArrived, 1) == ctas - 1;
+            if (is_last) a.scratch[kKvArrived] = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        if (!is_last) return;
+    }
+    // ---- the bookkeeping ----
+    __syncthreads();                                         // every thread has read the list of copies
+    // the lowest `total` free pages are taken: which entry's page is each?
+    int rank = free_before, e = -1;
     for (int w = w0; w < w1 && rank < total; ++w) {
         uint32_t bits = __ldcg(a.free + w), take = 0;
         for (; bits && rank < total; bits &= bits - 1, ++rank) {
+            const int page = 32 * w + __ffs(bits) - 1;
+            if (e < 0) {                                     // the last entry that begins at or in front of this rank
+                e = 0;
+                int hi = n;
+                while (hi - e > 1) {
+                    const int mid = (e + hi) / 2;
+                    (ahead[mid] <= rank ? e : hi) = mid;
+                }
+            }
+            while (rank >= ahead[e + 1]) ++e;
             take |= bits & -bits;
-            a.refs[32 * w + __ffs(bits) - 1] = 1;
+            a.refs[page] = 1;
+            const int s = seqs[e], c = counts ? counts[e] : m, len = a.lens[s];
+            const int fresh = pages_of(len + c, ps) - pages_of(len, ps), nth = rank - ahead[e];
+            const bool copied_too = ahead[e + 1] - ahead[e] > fresh;
+            if (copied_too && nth == 0) copies[e] = page;    // (the list of copies is done with)
+            else a.table[(long long)s * a.max_pages + pages_of(len, ps) + nth - copied_too] = page;
         }
         if (take) atomicAnd(a.free + w, ~take);
     }
-    __syncthreads();
-    for (int e = e0; e < e1; ++e) {
-        const int se = seqs[e], ce = counts ? counts[e] : m, oe = a.lens[se], to = __ldcg(a.scratch + kKvCopy + e);
-        if (to >= 0) {
-            int* slot = a.table + (long long)se * a.max_pages + oe / ps;
+    __syncthreads();                                         // the free bits and the old lengths were read
+#pragma unroll
+    for (int i = 0; i < kExtPer; ++i) {
+        if (i >= e1 - e0) continue;
+        if (copy[i]) {
+            int* slot = a.table + (long long)seq[i] * a.max_pages + old[i] / ps;
             drop_page(a, *slot);
-            *slot = to;
+            *slot = copies[e0 + i];
         }
-        a.lens[se] = oe + ce;
+        a.lens[seq[i]] = old[i] + count[i];
     }
 }
 
@@ -417,11 +458,7 @@ cudaError_t launch_kv_reset(const KvArgs& a, cudaStream_t stream)
 
 cudaError_t launch_kv_extend(const KvArgs& a, int n, int m, const int* seqs, const int* counts, cudaStream_t stream)
 {
-    int copiers = (148 + n - 1) / n;
-    if (copiers > 2 * a.n_layers * a.n_heads) copiers = 2 * a.n_layers * a.n_heads;
-    if (copiers > 16) copiers = 16;
-    return launch_pdl(kv_extend_kernel, dim3((unsigned)n, (unsigned)copiers), dim3(kExtThreads), seen_bytes(a), stream, a,
-                      n, m, seqs, counts);
+    return launch_pdl(kv_extend_kernel, dim3(148), dim3(kExtThreads), seen_bytes(a), stream, a, n, m, seqs, counts);
 }
 
 cudaError_t launch_kv_write(const KvArgs& a, int layer, int n, int m, const int* seqs, const int* counts,

@@ -364,20 +364,24 @@ def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Op
     for 8 everywhere.  Inference only: there is no backward pass."""
     squeeze = x.dim() == 1
     x2 = x.reshape(1, -1) if squeeze else x
-    if x2.dim() != 2 or packed.dim() != 4:
-        raise ValueError("expected x of (m, k_in) or (k_in,) and packed of (n_out/16, k_in/64, 32, 4)")
-    if not x.is_cuda:
-        raise ValueError(f"x: expected a tensor on the current CUDA device, got {x.device}")
+    device = x.get_device()
+    if x2.dim() != 2 or packed.dim() != 4 or device < 0 or device != torch.cuda.current_device():
+        raise ValueError("expected x of (m, k_in) or (k_in,) on the current CUDA device and packed of "
+                         "(n_out/16, k_in/64, 32, 4)")
     (m, k_in), tiles = x2.shape, packed.shape[0]
     n_out = 16 * tiles
     if group not in (32, 64, 128) or k_in % group or k_in % 64 or not 1 <= m <= 32:
         raise Exl3Error(EXL3_ERR_UNSUPPORTED, f"q4_gemm of {m} rows, k_in {k_in}, group {group}")
-    device = torch.cuda.current_device()
-    _expect(x2, "x", torch.float16, (m, k_in), device)
-    _expect(packed, "packed", torch.int32, (tiles, k_in // 64, 32, 4), device)
-    _expect(scale, "scale", torch.float16, (k_in // group, n_out), device)
-    if zero is not None:
-        _expect(zero, "zero", torch.uint8, (k_in // group, n_out), device)
+    groups = (k_in // group, n_out)
+    # one condition on the usual path: a call of a small product is bound by the host
+    if not (x2.dtype is torch.float16 and x2.is_contiguous() and packed.dtype is torch.int32 and
+            packed.shape == (tiles, k_in // 64, 32, 4) and packed.is_contiguous() and packed.get_device() == device and
+            scale.dtype is torch.float16 and scale.shape == groups and scale.is_contiguous() and
+            scale.get_device() == device and (zero is None or _dense(zero, torch.uint8, groups, device))):
+        _expect(x2, "x", torch.float16, (m, k_in), device)
+        _expect(packed, "packed", torch.int32, (tiles, k_in // 64, 32, 4), device)
+        _expect(scale, "scale", torch.float16, groups, device)
+        _expect(zero, "zero", torch.uint8, groups, device)
     if out is None:
         out = x2.new_empty((m, n_out), dtype=torch.float32) if fp32 else x2.new_empty((m, n_out))
     else:
