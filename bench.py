@@ -55,6 +55,8 @@ def parse():
     ap.add_argument("--separate", action="store_true", help="one library call per matrix instead of per layer")
     ap.add_argument("--no-graph", action="store_true")
     ap.add_argument("--no-extra", action="store_true", help="time only the main row count (no M=1/8/16, no chain)")
+    ap.add_argument("--context", type=int, default=None,
+                    help="also time the chained stack with attention over a paged cache that holds this many tokens")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--ref-budget", type=float, default=None,
                     help="seconds of oracle work per step for --impl reference (default: about 90 s per run)")
@@ -410,6 +412,15 @@ def run_ours(args, world, rank, local):
             chain[m] = rank_max(timed(torch, fn, args.steps, args.warmup, barrier))
             assert ex.workspace_status(st.ws) == ex.EXL3_OK
             del g, st
+    context_chain = {}
+    if args.context is not None and full_layers:
+        for m in ([args.m, 1] if args.m != 1 else [1]):
+            st = Stack(ex, torch, device, m, specs, weights, mode="chain", context=args.context)
+            fn, g, launch = graph_or_eager(st, st.run)
+            context_chain[m] = rank_max(timed(torch, fn, args.steps, args.warmup, barrier))
+            assert ex.workspace_status(st.ws) == ex.EXL3_OK
+            st.cache.check()
+            del g, st
 
     configs = time_configs(torch, ex, device, args.steps, args.warmup) if extra and rank == 0 and world == 1 else None
 
@@ -509,6 +520,8 @@ def run_ours(args, world, rank, local):
         line["step_vs_m1"] = {("m%d" % m): round(r["ms"] / m1_ms, 3) for m, r in results.items() if m != 1}
     for m, ms in chain.items():
         line["us_per_layer_chain_m%d" % m] = round(ms * 1e3 / layers, 3)
+    for m, ms in context_chain.items():
+        line["us_per_layer_chain_context%d_m%d" % (args.context, m)] = round(ms * 1e3 / layers, 3)
     if configs:
         line["configs_2_to_4"] = configs
     if main["clocks"]:

@@ -7,7 +7,7 @@
 
 #include "../../include/exl3.h"
 #include "exl3_common.cuh"
-#include "exl3_internal.h"
+#include "exl3_cache.h"
 
 namespace {
 

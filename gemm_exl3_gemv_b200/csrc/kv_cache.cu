@@ -10,7 +10,7 @@
 // out for itself from data that no CTA of the call changes before the last one
 // has read it; no CTA waits for another.
 #include "exl3_common.cuh"
-#include "exl3_internal.h"
+#include "exl3_cache.h"
 
 namespace exl3 {
 

@@ -36,7 +36,7 @@
 
 #include <type_traits>
 
-#include "exl3_internal.h"
+#include "exl3_cache.h"
 #include "exl3_tc.cuh"
 
 namespace exl3 {

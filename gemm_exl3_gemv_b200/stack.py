@@ -22,6 +22,13 @@ Two ways to chain the layer's seven matrices (q, k, v, o, gate, up, down):
   ``grouped=True`` they run as one grouped call: two dependent steps per
   layer (three with ``grouped=False``).
 
+  With ``context=N`` the chain has its attention: the m rows are the newest
+  tokens of one sequence whose first N tokens lie in a paged cache
+  (``kvcache.KvCache``, synthetic keys and values).  A step drops the tokens
+  that the last one drafted and makes room for m new ones; in every layer k's
+  and v's outputs are written to the cache, and o takes the attention of q's
+  output over it.
+
 Buffers: inputs and outputs of all products live in one flat device buffer
 each (x and y), a layer's slices contiguous, so an end-to-end step moves one
 slice per layer between pinned host memory and the device.
@@ -75,10 +82,15 @@ class Stack:
     runs).  ``large``: use the many-row call (default: m > 32).  ``run_e2e``
     moves every layer's x and y slices, so it is meant for the sweep."""
 
+    HEAD_DIM = 128                # of the attention (context runs)
+
     def __init__(self, ex, torch, device, m: int, specs, weights, mode: str = "sweep",
-                 grouped: bool = True, large: Optional[bool] = None):
+                 grouped: bool = True, large: Optional[bool] = None, context: Optional[int] = None,
+                 page_size: int = 64):
         if mode not in ("sweep", "chain"):
             raise ValueError(mode)
+        if context is not None and (mode != "chain" or context < 0 or not 1 <= m <= 32):
+            raise ValueError("a context needs a chained stack of up to 32 rows")
         self.ex, self.torch, self.device = ex, torch, device
         self.m, self.mode = m, mode
         self.large = (m > 32) if large is None else large
@@ -123,6 +135,8 @@ class Stack:
                 h = lay.by_kind("q").spec
                 if any(p.spec.bits != h.bits for p in lay.products):
                     raise ValueError("a chained layer has one bit width")
+        self.context = context
+        self.cache = None if context is None else self._make_cache(context, page_size)
         self.ws = torch.zeros(self._workspace_bytes(), dtype=torch.uint8, device=device)
         self.s_in = torch.cuda.Stream(device=device)
         self.s_out = torch.cuda.Stream(device=device)
@@ -130,6 +144,41 @@ class Stack:
         self.io_bytes = sum(2 * m * (s.k_in + s.n_out) + 2 * (s.k_in + 2 * s.n_out) for s in self.specs)
         self.h2d = self.x_pin.numel() * 2
         self.d2h = self.y_pin.numel() * 2
+
+    # ---------------------------------------------------------- context ---
+
+    def _make_cache(self, context, page_size):
+        """A cache of all layers that holds one sequence of ``context`` tokens
+        (normal keys and values, seeded), with room for m more."""
+        from .kvcache import KvCache
+        torch, d = self.torch, self.HEAD_DIM
+        layer = self.layers[0]
+        self.q_heads, kv_heads = layer.by_kind("q").spec.n_out // d, layer.by_kind("k").spec.n_out // d
+        shapes = {(lay.by_kind("q").spec.n_out, lay.by_kind("k").spec.n_out, lay.by_kind("v").spec.n_out) for lay in self.layers}
+        if shapes != {(self.q_heads * d, kv_heads * d, kv_heads * d)} or self.q_heads % kv_heads:
+            raise ValueError(f"attention needs layers with the same whole heads of {d} channels in q, k and v")
+        pages = -(-(context + self.m) // page_size)
+        cache = KvCache.empty(len(self.layers), pages, kv_heads, page_size, d, 1, pages, device=self.device)
+        self.seqs = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.kept = torch.full((1,), context, dtype=torch.int32, device=self.device)
+        if context:
+            cache.extend(self.seqs, context)
+            g = torch.Generator(device=self.device)
+            g.manual_seed(11)
+            cache.k.normal_(generator=g)
+            cache.v.normal_(generator=g)
+        self.att = torch.empty((1, self.m, self.q_heads, d), dtype=torch.float16, device=self.device)
+        return cache
+
+    def _attend(self, li):
+        """Layer li's attention: its k and v rows go to the cache, its q rows
+        attend to it; the result is o's input."""
+        P = {p.kind: p for p in self.layers[li].products}
+        c, d = self.cache, self.HEAD_DIM
+        rows = lambda y: y.view(1, self.m, -1, d)
+        c.write(li, self.seqs, rows(P["k"].y), rows(P["v"].y))
+        c.attention(li, self.seqs, rows(P["q"].y), out=self.att, workspace=self.ws)
+        return self.att.view(self.m, -1)
 
     # ------------------------------------------------------------ sizes ---
 
@@ -166,6 +215,8 @@ class Stack:
             else:
                 n = ex.grouped_workspace_bytes(m, [(p.spec.k_in, p.spec.n_out) for p in pl], pl[0].spec.bits)
             need = max(need, n)
+        if self.cache is not None:
+            need = max(need, self.cache.attention_workspace(1, m, self.q_heads).numel())
         return need
 
     def launches(self) -> int:
@@ -180,6 +231,8 @@ class Stack:
                 total += ex.kernel_launches(m, s.k_in, sum(p.spec.n_out for p in pl), s.bits)
             else:
                 total += ex.grouped_kernel_launches(m)
+        if self.cache is not None:                      # truncate and extend; write and attention per layer
+            total += 2 + 2 * len(self.layers)
         return total
 
     # -------------------------------------------------------------- run ---
@@ -201,12 +254,13 @@ class Stack:
             ex.gemm_siblings(h, q.su, [(p.packed, p.scale, p.sv) for p in sib], q.spec.bits,
                              outs=[p.y for p in sib], workspace=self.ws)
             o, d = P["o"], P["down"]
+            att = P["q"].y if self.cache is None else self._attend(li)
             if self.grouped:
-                ex.gemm_grouped([(P["q"].y, o.packed, o.scale, o.su, o.sv, o.y),
+                ex.gemm_grouped([(att, o.packed, o.scale, o.su, o.sv, o.y),
                                  (P["up"].y, d.packed, d.scale, d.su, d.sv, d.y)],
                                 o.spec.bits, workspace=self.ws)
             else:
-                ex.gemm(P["q"].y, o.packed, o.scale, o.su, o.sv, o.spec.bits, out=o.y, workspace=self.ws)
+                ex.gemm(att, o.packed, o.scale, o.su, o.sv, o.spec.bits, out=o.y, workspace=self.ws)
                 ex.gemm(P["up"].y, d.packed, d.scale, d.su, d.sv, d.spec.bits, out=d.y, workspace=self.ws)
             return
         if self.grouped:
@@ -218,6 +272,9 @@ class Stack:
             call(p.x, p.packed, p.scale, p.su, p.sv, p.spec.bits, out=p.y, workspace=self.ws)
 
     def run(self):
+        if self.cache is not None:
+            self.cache.truncate(self.seqs, self.kept)
+            self.cache.extend(self.seqs, self.m)
         for li in range(len(self.layers)):
             self.run_layer(li)
 

@@ -138,3 +138,62 @@ def test_graphed_chain_matches_composed_oracle(oracle_mod, m, grouped):
         assert mx <= d * gpu_helpers.MAX_ABS, f"chain {p.spec.name} m={m} grouped={grouped} depth {d}: max-abs {mx:.3e}"
     # the chain is carried: layer 1's input is layer 0's down output
     assert np.abs(ref["l1.down"]).max() > 0
+
+
+def _oracle_context_chain(oracle_mod, st, m, layers):
+    """The chained step with attention: as _oracle_chain, with o's input the fp64 attention of q's rows over the
+    cache's first tokens and the layer's own k and v rows (rounded to fp16, as the library stores them)."""
+    import cache_model
+    inp = {s.name: synth.make_inputs(s, chain=True) for s in st.specs}
+    spec = {s.name: s for s in st.specs}
+    out, n, d = {}, st.context, st.HEAD_DIM
+    h = inp["l0.q"].x[:m]
+    pages = st.cache.table[0].cpu().numpy()
+    k_all, v_all = (x.cpu().numpy() for x in (st.cache.k, st.cache.v))
+    for l in range(layers):
+        su = inp[f"l{l}.q"].su
+        product = lambda kind, x, su: oracle_mod.gemm(x, inp[f"l{l}.{kind}"].packed, inp[f"l{l}.{kind}"].scale, su,
+                                                      inp[f"l{l}.{kind}"].sv, spec[f"l{l}.{kind}"].k_in,
+                                                      spec[f"l{l}.{kind}"].n_out, spec[f"l{l}.{kind}"].bits)
+        for kind in ("q", "k", "v", "gate", "up"):
+            out[f"l{l}.{kind}"] = product(kind, h, su)
+        half = lambda kind: out[f"l{l}.{kind}"].astype(np.float16).astype(np.float64).reshape(m, -1, d)
+        past = lambda a: np.concatenate([a[l, p] for p in pages], 1)[:, :n].transpose(1, 0, 2).astype(np.float64)
+        keys, values = (np.concatenate([past(a), half(kind)], 0) for a, kind in ((k_all, "k"), (v_all, "v")))
+        att = cache_model.attention(half("q"), keys, values, n, d ** -0.5)[0]
+        out[f"l{l}.att"] = att.reshape(m, -1)
+        out[f"l{l}.o"] = product("o", out[f"l{l}.att"].astype(np.float16), inp[f"l{l}.o"].su)
+        out[f"l{l}.down"] = product("down", out[f"l{l}.up"].astype(np.float16), inp[f"l{l}.down"].su)
+        h = out[f"l{l}.down"].astype(np.float16)
+    return out
+
+
+@pytest.mark.parametrize("m,context", [(1, 200), (32, 77), (8, 0)])
+def test_graphed_chain_with_attention_matches_composed_oracle(oracle_mod, m, context):
+    """The chained stack over a cache: products, cache growth, writes and attention of two layers in one graph,
+    replayed twice (each replay drops the drafted tokens of the one before).  Tolerances: as for the chain, for
+    the products before the attention; behind it, the attention's inputs are off by the depth's 1e-3 each (q, k
+    and v).  A relative error e of q and k moves a score by up to 2 e |s|, and a probability by as much; with
+    rows of about 128 normal products a score is a few units, so o is within 1e-3 (v) + 2 * 8 * 1e-3 (scores up
+    to 8) of the exact attention, and o's product passes that on."""
+    import gpu_helpers
+    import torch
+    from gemm_exl3_gemv_b200 import exl3 as ex
+    from gemm_exl3_gemv_b200.stack import Stack
+    layers = 2
+    specs = [s for s in synth.workload(5, m=32) if s.layer < layers]
+    weights = [synth.splitmix64_words_torch(s.stream_id, s.n_words, "cuda") for s in specs]
+    st = Stack(ex, torch, torch.device("cuda"), m, specs, weights, mode="chain", context=context)
+    st.run()
+    torch.cuda.synchronize()
+    _replay(st)
+    st.cache.check()
+    assert st.cache.lens.tolist() == [context + m]
+    ref = _oracle_context_chain(oracle_mod, st, m, layers)
+    for p in st.products:
+        layer, kind = p.spec.layer, p.spec.name.split(".")[1]
+        depth = 2 * layer + (2 if kind in ("o", "down") else 1)
+        got, r = p.y.cpu().numpy().astype(np.float64), ref[p.spec.name]
+        tol = depth * gpu_helpers.REL_L2 + (17 * depth * gpu_helpers.REL_L2 if kind == "o" else 0)
+        rel = np.linalg.norm(got - r) / np.linalg.norm(r)
+        assert np.all(np.isfinite(got)) and rel <= tol, f"{p.spec.name} m={m} context={context}: rel-L2 {rel:.3e}"
