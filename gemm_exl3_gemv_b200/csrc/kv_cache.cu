@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int 
 {
     grid_dep_wait();
     grid_dep_launch();
-    if (__ldcg(a.scratch + kKvFault)) return;
+    const int old_fault = __ldcg(a.scratch + kKvFault);      // looked at once the places' loads are on their way
     const int row_vec = a.n_heads * a.head_dim / 8, head_vec = a.head_dim / 8, ps = a.page_size;
     const long long all = (long long)n * m * row_vec;
     const long long page_el = (long long)a.n_heads * ps * a.head_dim;
@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int 
         const long long r = i / row_vec;
         const int b = (int)(r / m), row = (int)(r % m);
         const int c = counts ? counts[b] : m, s = seqs[b];
+        if (old_fault) return;
         if (row >= c) continue;
         if (c > m || s < 0 || s >= a.n_seqs) { fault(a, kKvIndex); continue; }
         const int pos = a.lens[s] - c + row;
@@ -458,7 +459,7 @@ cudaError_t launch_kv_reset(const KvArgs& a, cudaStream_t stream)
 
 cudaError_t launch_kv_extend(const KvArgs& a, int n, int m, const int* seqs, const int* counts, cudaStream_t stream)
 {
-    return launch_pdl(kv_extend_kernel, dim3(148), dim3(kExtThreads), seen_bytes(a), stream, a, n, m, seqs, counts);
+    return launch_pdl(kv_extend_kernel, dim3(148 * 3), dim3(kExtThreads), seen_bytes(a), stream, a, n, m, seqs, counts);
 }
 
 cudaError_t launch_kv_write(const KvArgs& a, int layer, int n, int m, const int* seqs, const int* counts,

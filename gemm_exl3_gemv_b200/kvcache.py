@@ -113,6 +113,11 @@ class KvCache:
                              f"8 elements apart; strides are {t.stride()}")
         return m, s0, s1
 
+    @staticmethod
+    def _alike(t: torch.Tensor, other: torch.Tensor) -> bool:
+        return t.dtype is other.dtype and t.shape == other.shape and t.stride() == other.stride() and \
+            t.get_device() == other.get_device()
+
     def _where(self, stream):
         """The stream's handle; the cache's device must be the current one."""
         if torch.cuda.current_device() != self._index:
@@ -149,10 +154,9 @@ class KvCache:
         counts[b]) tokens of each sequence, in one layer."""
         p, n = self._list(seqs, "seqs"), seqs.shape[0]
         c = self._list(counts, "counts", n)
-        rows = self._rows(k, "k", n, self.n_heads)
-        if self._rows(v, "v", n, self.n_heads) != rows:
-            raise ValueError("k and v must have the same shape and strides")
-        m, bs, rs = rows
+        m, bs, rs = self._rows(k, "k", n, self.n_heads)
+        if not self._alike(v, k):
+            raise ValueError("k and v must have the same type, device, shape and strides")
         s = self._where(stream)
         if n and m:
             ex._check(ex.lib.exl3_kv_write(self._ref, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s),
@@ -206,9 +210,12 @@ class KvCache:
         if out is None:
             make = torch.empty if counts is None else torch.zeros
             out = make((n, m, heads, self.head_dim), dtype=torch.float16, device=self.device)
-        mo, ob, orow = self._rows(out, "out", n, heads)
-        if mo != m:
-            raise ValueError(f"out: expected {m} rows per sequence, got {mo}")
+        if self._alike(out, q):
+            ob, orow = qb, qr
+        else:
+            mo, ob, orow = self._rows(out, "out", n, heads)
+            if mo != m:
+                raise ValueError(f"out: expected {m} rows per sequence, got {mo}")
         if lse is not None:
             ex._expect(lse, "lse", torch.float32, (n, m, heads), self._index)
         s = self._where(stream)
