@@ -614,8 +614,9 @@ extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int
     t.n_q_heads = n_q_heads;
     t.group = n_q_heads / t.c.n_heads;
     t.scale = scale;
-    t.window = window;
-    t.sinks = sinks;
+    // no sequence is longer than 2^30 tokens: more is the same, and sums of positions stay in 32 bits
+    t.window = window < (1 << 30) ? window : 1 << 30;
+    t.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
     t.out = out;
     t.o_bs = out_batch_stride;
     t.o_rs = out_row_stride;

@@ -1,0 +1,412 @@
+// paged_attn.cuh -- what the two attention kernels (paged_attn.cu: up to 16
+// rows per sequence and head, paged_attn_tc.cu: more) share: how the work is
+// cut, the producer warp that brings it to shared memory, and the join of
+// partial results.
+//
+// A group is a (sequence, head of the cache, row tile); its work is the
+// 64-token tiles its rows see (a window skips the tiles in between).  The tiles
+// of all groups, in order, are cut into equal contiguous ranges, one per CTA,
+// so the lengths may be as ragged as they like; the cut is worked out on the
+// device from the lengths.  A group that several CTAs share is joined by the
+// last of them to arrive, in the order of the ranges, in two levels when they
+// are many.  (Ranges that CTAs take as they get done were measured too: the
+// equal shares of a 131077-token sequence are done between 66 and 100 us, but
+// each further stretch cost more than the even finish gave.)
+#pragma once
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "exl3_cache.h"
+#include "exl3_tc.cuh"
+
+namespace exl3 {
+
+namespace attn {
+
+constexpr int kTile = 64;                                    // tokens per tile
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMinTiles = 2;                                 // of a CTA's share, from which another CTA is worth its part of the join
+constexpr int kFan = 8;                                      // parts joined at once
+constexpr int kMaxCtas = 148 * 2;
+
+struct AttnPlan {
+    int row_tiles, tile_rows; // row tiles of a (sequence, head), and their rows
+    int entries;              // sequences x row tiles
+    int page_shift;
+    float scale_log2;
+};
+
+// How the tiles of all groups are cut: the first `more` ranges have one tile
+// more than `share`.
+struct AttnCut {
+    int ranges, share, more;
+    __device__ __forceinline__ AttnCut(int total, int ctas)
+    {
+        ranges = min(ctas, (total + kMinTiles - 1) / kMinTiles);
+        share = total / ranges;
+        more = total - share * ranges;
+    }
+    __device__ __forceinline__ int first(int r) const { return r * share + min(r, more); }
+    __device__ __forceinline__ int range_of(int tile) const
+    {
+        const int border = more * (share + 1);
+        return tile < border ? tile / (share + 1) : more + (tile - border) / share;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 0xffff for each half of the pair that is finite (x * 0 is NaN for the others)
+__device__ __forceinline__ uint32_t finite_halves(uint32_t u)
+{
+    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(0.f));
+    return __heq2_mask(z, z);
+}
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+
+// What an entry (sequence b of the list, row tile) has to do.
+struct Entry {
+    int seq, len, count;      // len: tokens, the new ones included
+    int row0, rows;           // rows of the tile (row r: token r / G, head r % G)
+    int sink_tiles;           // leading tiles that only the sinks need
+    int tile0;                // first tile of the window
+    int tiles;                // all of them
+};
+
+__device__ __forceinline__ Entry entry_of(const AttnArgs& a, const AttnPlan& pl, int e)
+{
+    Entry r;
+    const int b = e / pl.row_tiles, rt = e % pl.row_tiles;
+    const int c = a.counts ? min(max(a.counts[b], 0), a.m) : a.m;
+    r.seq = a.seqs[b];
+    r.count = c;
+    r.row0 = rt * pl.tile_rows;
+    r.rows = min(c * a.group - r.row0, pl.tile_rows);
+    r.sink_tiles = r.tile0 = r.tiles = r.len = 0;
+    if (r.seq < 0 || r.seq >= a.c.n_seqs) {
+        atomicOr(a.c.scratch + kKvFault, kKvIndex);
+        r.rows = 0;
+    }
+    if (r.rows <= 0) { r.rows = 0; return r; }
+    r.len = min(max(a.c.lens[r.seq], 0), a.c.max_pages << pl.page_shift);
+    const int p0 = r.len - c + r.row0 / a.group, p1 = r.len - c + (r.row0 + r.rows - 1) / a.group;
+    const int hi = max(p1 + 1, 0);                           // tokens [lo, hi) and the sinks
+    const int lo = a.window && p0 >= a.window ? p0 - a.window + 1 : 0;
+    r.tile0 = lo / kTile;
+    r.sink_tiles = min((int)(((long long)a.sinks + kTile - 1) / kTile), r.tile0);
+    r.tiles = max(1, r.sink_tiles + (hi + kTile - 1) / kTile - r.tile0);
+    return r;
+}
+
+__device__ __forceinline__ int tile_at(const Entry& e, int i) { return i < e.sink_tiles ? i : e.tile0 + i - e.sink_tiles; }
+
+// What the producer tells the consumers: the next stretch is n tiles from tile
+// off on of head h of an entry, whose group's first tile is gstart.  n = 0:
+// there are no more.
+struct Stretch {
+    Entry en;
+    int b, h, n, off, gstart, first;     // first: the first of this CTA's stretches
+};
+
+// The tiles in front of every thread's entries, in front[0..THREADS); returns
+// all of them.  The whole block; `sums`: a word per warp.
+template <int THREADS>
+__device__ __forceinline__ int count_tiles(const AttnArgs& a, const AttnPlan& pl, int* front, int* sums)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (pl.entries + THREADS - 1) / THREADS;
+    int incl = 0;
+    const int e_end = min(pl.entries, (tid + 1) * per);
+    for (int e = tid * per; e < e_end; ++e) incl += a.c.n_heads * entry_of(a, pl, e).tiles;
+    const int mine = incl;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    front[tid] = before;
+    __syncthreads();
+    return total;
+}
+
+// Waits that give up: after the first that runs out the others return at once.
+struct Patience {
+    uint32_t* status;
+    bool alive;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity)
+    {
+        if (!alive) return;
+        alive = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+        if (!alive && (threadIdx.x & 31) == 0) atomicOr(status, kStatusTimeout);
+    }
+};
+
+// Stage and phase of a ring.
+template <int N>
+struct Turn {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The ring of tiles, and the notes about stretches, in shared memory.
+struct Pipes {
+    unsigned char* ring;
+    uint64_t *full, *empty;              // per stage
+    uint64_t *told, *heard;              // two stretches in turn, and when they are read
+    Stretch* notes;
+};
+
+// The producer warp: walks the CTA's range, tells what the stretches are and
+// brings their tiles (TMA, one box per page part and 64 columns, 128-byte
+// swizzle).  Its reads of lengths and tables run ahead of the work: with the
+// memory saturated, each dependent read takes 2 us.  queries(stretch, its
+// entry): called once per stretch, before its tiles.
+template <int D, int STAGES, int THREADS, typename Queries>
+__device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const CUtensorMap* kmap,
+                                        const CUtensorMap* vmap, const int* front, const Pipes& io, Patience& p, Queries queries)
+{
+    constexpr int kHalf = kTile * D * 2;                     // bytes of a tile's keys (or values)
+    const int lane = threadIdx.x & 31, heads = a.c.n_heads, per = (pl.entries + THREADS - 1) / THREADS;
+    Turn<STAGES> stage;
+    Turn<2> note;
+    int u = cut.first(blockIdx.x);
+    const int u1 = cut.first(blockIdx.x + 1);
+    // the entry that tile u belongs to: of the last thread whose entries begin at or in front of it
+    int behind = -1;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) behind += __popc(__ballot_sync(0xffffffffu, front[32 * i + lane] <= u));
+    int base = front[behind], e = behind * per;
+    Entry en = entry_of(a, pl, e);
+    const int ps = 1 << pl.page_shift, parts = ps >= kTile ? 1 : kTile / ps, part_rows = ps < kTile ? ps : kTile;
+    for (bool first = true; u < u1; first = false) {
+        while (u >= base + heads * en.tiles) {
+            base += heads * en.tiles;
+            en = entry_of(a, pl, ++e);
+        }
+        const int h = (u - base) / en.tiles, off = (u - base) - h * en.tiles;
+        const int n = min(en.tiles - off, u1 - u), b = e / pl.row_tiles;
+        p.wait(io.heard + note.at, note.phase ^ 1);
+        const Stretch st = {en, b, h, n, off, u - off, first};
+        if (lane == 0) {
+            io.notes[note.at] = st;
+            mbar_arrive(io.told + note.at);
+        }
+        __syncwarp();
+        note.next();
+        queries(st);
+        const int* row = a.c.table + (long long)en.seq * a.c.max_pages;
+        const int held = (en.len + ps - 1) >> pl.page_shift;
+        for (int i0 = 0; i0 < n; i0 += 32 / parts) {
+            // each lane looks up the page of one tile part
+            const int i = i0 + lane / parts, part = lane % parts;
+            int page = -1, token = 0;
+            if (i < n) {
+                token = tile_at(en, off + i) * kTile + part * part_rows;
+                const int j = token >> pl.page_shift;
+                if (j < held) {
+                    page = row[j];
+                    if (page < 0 || page >= a.c.n_pages) {
+                        page = -1;
+                        atomicOr(a.c.scratch + kKvFault, kKvIndex);
+                    }
+                }
+            }
+            const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+            for (int k = 0; k < 32 / parts && i0 + k < n; ++k) {
+                p.wait(io.empty + stage.at, stage.phase ^ 1);
+                if (!p.alive) continue;                      // no more copies; the consumers give up as well
+                const uint32_t mask = (good >> (k * parts)) & ((1u << parts) - 1);
+                unsigned char* kt = io.ring + stage.at * 2 * kHalf;
+                if (lane == 0) mbar_arrive_expect_tx(io.full + stage.at, __popc(mask) * part_rows * D * 4);
+                __syncwarp();
+                if (lane / parts == k && page >= 0) {
+                    const int y = ((page * heads + h) << pl.page_shift) + (token & (ps - 1));
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        const int at = x * kTile * 128 + part * part_rows * 128;
+                        tma_box(kt + at, kmap, 64 * x, y, io.full + stage.at);
+                        tma_box(kt + kHalf + at, vmap, 64 * x, y, io.full + stage.at);
+                    }
+                }
+                __syncwarp();
+                stage.next();
+            }
+        }
+        u += n;
+    }
+    p.wait(io.heard + note.at, note.phase ^ 1);
+    if (lane == 0) {
+        io.notes[note.at].en.rows = 0;
+        io.notes[note.at].n = 0;
+        mbar_arrive(io.told + note.at);
+    }
+}
+
+// Counts the calling CTA in; true in the last of `of` CTAs, which may then read
+// what the others wrote before they were counted.  Consumer threads: the
+// barriers order the other threads' accesses around the first one's fences.
+__device__ __forceinline__ bool last_of(uint32_t* counter, int of, int& flag, int tid, int threads)
+{
+    named_bar(1, threads);
+    if (tid == 0) {
+        __threadfence();
+        flag = atomicAdd(counter, 1u) == (uint32_t)of - 1;
+        if (flag) *counter = 0;
+        __threadfence();
+    }
+    named_bar(1, threads);
+    return flag;
+}
+
+// Parts of a group, joined by the consumers of one CTA in the order of the
+// parts: written out (last), or to the first part's slot.  A thread takes a
+// float4 of kAcc rows, with kDeep parts in flight (the parts lie in the L2;
+// their latency is the cost), and rescales by the rows' maxima as it goes.
+template <typename S, int D, typename SlotOf>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, int b, int h, float* slots, int parts,
+                                           SlotOf slot_of, bool last, int tid)
+{
+    constexpr int kVec = D / 4, kStep = S::kConsumers / kVec;    // rows apart
+    constexpr int kAcc = S::kRows / kStep < 4 ? S::kRows / kStep : 4, kDeep = 4;
+    static_assert(S::kRows % (kStep * kAcc) == 0);
+    auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
+    const int col = 4 * (tid % kVec);
+    for (int base = 0; base < en.rows; base += kStep * kAcc) {
+        const int r0 = base + tid / kVec;
+        float4 acc[kAcc];
+        float mx[kAcc], sum[kAcc];
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) {
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            mx[i] = kNegInf;
+            sum[i] = 0.f;
+        }
+        for (int c0 = 0; c0 < parts; c0 += kDeep) {
+            float4 v[kDeep][kAcc];
+            float2 ms[kDeep][kAcc];
+#pragma unroll
+            for (int c = 0; c < kDeep; ++c) {
+                const float* from = part_of(c0 + c);
+#pragma unroll
+                for (int i = 0; i < kAcc; ++i) {
+                    const float* at = from + (r0 + i * kStep) * S::kSlotRow;
+                    const bool in = c0 + c < parts;
+                    v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(at + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ms[c][i] = in ? __ldcg(reinterpret_cast<const float2*>(at + D)) : make_float2(kNegInf, 0.f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAcc; ++i) {
+                float now = mx[i];
+#pragma unroll
+                for (int c = 0; c < kDeep; ++c) now = fmaxf(now, ms[c][i].x);
+                const float at = now == kNegInf ? 0.f : now, f0 = ex2(mx[i] - at);
+                mx[i] = now;
+                sum[i] *= f0;
+                acc[i].x *= f0, acc[i].y *= f0, acc[i].z *= f0, acc[i].w *= f0;
+#pragma unroll
+                for (int c = 0; c < kDeep; ++c) {
+                    const float f = ex2(ms[c][i].x - at);
+                    sum[i] += f * ms[c][i].y;
+                    acc[i].x += f * v[c][i].x;
+                    acc[i].y += f * v[c][i].y;
+                    acc[i].z += f * v[c][i].z;
+                    acc[i].w += f * v[c][i].w;
+                }
+            }
+        }
+        // row maxima of the first part are read by other threads until here
+        if (!last) named_bar(1, S::kConsumers);
+#pragma unroll
+        for (int i = 0; i < kAcc; ++i) {
+            const int r = r0 + i * kStep;
+            if (last) {
+                if (r >= en.rows) break;
+                const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr - tok * a.group;
+                const bool none = en.len - en.count + tok < 0;    // a row that sees no token: zeros
+                const float inv = none ? 0.f : 1.f / sum[i];
+                *reinterpret_cast<uint2*>(a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D + col) =
+                    make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
+                if (a.lse && col == 0)
+                    a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] = none ? kNegInf : (mx[i] + (log2f(sum[i]) - S::kUp)) * kLn2;
+            } else {
+                float* at = part_of(0) + r * S::kSlotRow;
+                __stcg(reinterpret_cast<float4*>(at + col), acc[i]);
+                if (col == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
+            }
+        }
+    }
+}
+
+// Which of a CTA's stretches' slots, and counting in after the partial result
+// is written there: joins what is complete.  Consumer threads.
+template <typename S, int D>
+__device__ __forceinline__ float* slot_at(const AttnArgs& a, const Stretch& st)
+{
+    return reinterpret_cast<float*>(a.ws + ws_data_off()) + (long long)(2 * blockIdx.x + (st.first ? 0 : 1)) * S::kSlot;
+}
+template <typename S, int D>
+__device__ __forceinline__ void count_in(const AttnArgs& a, const AttnCut& cut, const Stretch& st, int& flag, int tid)
+{
+    float* slots = reinterpret_cast<float*>(a.ws + ws_data_off());
+    uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off());
+    // the group's parts: the first one is its range's first or last stretch, the others first ones
+    const int r_first = cut.range_of(st.gstart), parts = cut.range_of(st.gstart + st.en.tiles - 1) - r_first + 1;
+    const int late = st.gstart == cut.first(r_first) ? 0 : 1;
+    auto slot_of = [&](int c) { return 2 * (r_first + c) + (c == 0 ? late : 0); };
+    // up to kFan parts are joined at once, more in two levels of about the square root
+    int fan = parts;
+    if (parts > kFan)
+        for (fan = kFan / 2; fan * fan < parts; ++fan) {}
+    const int node = ((int)blockIdx.x - r_first) / fan * fan;
+    int from = node, step = 1, count = min(fan, parts - node);
+    uint32_t* counter = counters + slot_of(node);
+    while (last_of(counter, count, flag, tid, S::kConsumers)) {
+        const bool last = step == fan || fan == parts;
+        join_parts<S, D>(a, st.en, st.b, st.h, slots, count, [&](int c) { return slot_of(from + c * step); }, last, tid);
+        if (last) break;
+        from = 0;
+        step = fan;
+        count = (parts + fan - 1) / fan;
+        counter = counters + 2 * kMaxCtas + slot_of(0);
+    }
+}
+
+}  // namespace attn
+
+// The launch of the kernel for more than 16 rows (paged_attn_tc.cu).
+cudaError_t launch_attention_tc(const AttnArgs& a, const attn::AttnPlan& pl, int ctas, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, cudaStream_t stream);
+size_t attention_tc_slot_floats(int head_dim);
+
+}  // namespace exl3

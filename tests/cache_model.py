@@ -114,8 +114,9 @@ def attention(q, k, v, first, scale, window=0, sinks=0):
               by at most 2^-22 of the sum of magnitudes), scaled and taken to
               base 2 (two roundings of 2^-24 each, of the score): d
       p       e^(score) relative: 2 d (its own and the maximum's) + 2^-21, then
-              half a step of fp16, 2^-11; below 2^-28 of the largest it is no
-              normal number: 2^-38 of the largest, absolute
+              half a step of fp16, 2^-11; it carries a factor of 2^7 or more, so
+              below 2^-21 of the largest it is no normal number: half a step of
+              2^-24 over that factor, 2^-32 of the largest, absolute
       o       sums of up to n terms in fp32: n/16 + 8 steps of 2^-22 of the sum
               of magnitudes, for o and for the divisor; the result half a step
               of fp16 (2^-11, at least 2^-25 absolute)
@@ -139,6 +140,6 @@ def attention(q, k, v, first, scale, window=0, sinks=0):
             steps = (len(s) / 16 + 8) * 2.0 ** -22
             mag = p @ np.abs(vv) / total
             o_tol[i, h] = mag * (2.0 ** -11 + 4 * ds + 2 * 2.0 ** -21 + 2 * steps) + \
-                2.0 ** -38 * np.abs(vv).sum(0) / total + 2.0 ** -11 * np.abs(o[i, h]) + 2.0 ** -25
+                2.0 ** -32 * np.abs(vv).sum(0) / total + 2.0 ** -11 * np.abs(o[i, h]) + 2.0 ** -25
             lse_tol[i, h] = 2 * ds + 2.0 ** -21 + steps + 2.0 ** -22 * (1 + abs(lse[i, h]))
     return o, lse, o_tol, lse_tol
