@@ -586,6 +586,15 @@ extern "C" size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int
     return exl3::attention_workspace_bytes(m, n_q_heads, n_heads, head_dim);
 }
 
+extern "C" int exl3_paged_attention_launches(const exl3_kv_cache_t* cache, int n, int m, int n_q_heads)
+{
+    exl3::KvArgs a;
+    if (cache_args(cache, a) != EXL3_OK || n <= 0 || n > exl3::kKvMaxList || m <= 0 || m > 32 || n_q_heads <= 0 ||
+        !attention_heads_ok(n_q_heads, a.n_heads))
+        return 0;
+    return exl3::attention_launches(a, n, m, n_q_heads / a.n_heads);
+}
+
 extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int n, int m, const int32_t* seqs,
                                     const int32_t* counts, const uint16_t* q, long long q_batch_stride,
                                     long long q_row_stride, int n_q_heads, float scale, int window, int sinks,

@@ -84,6 +84,7 @@ struct AttnArgs {
 };
 size_t attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
 bool attention_tiles_ok(const AttnArgs& a);   // tiles are counted in 32 bits
+int attention_launches(const KvArgs& c, int n, int m, int group);
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace exl3

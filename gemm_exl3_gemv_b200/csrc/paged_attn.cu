@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
                         pos[i] < 0 ? kNegInf : (mx[i] + (log2f(sum[i]) - S::kUp)) * kLn2;
             }
         } else {
-            // ---- partial result to this stretch's slot; the last CTA of the group joins ----
-            float* slot = slot_at<S, D>(a, st);
+            // ---- partial result to this stretch's slot ----
+            float* slot = slot_at<S>(a, st);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float* at = slot + (g + 8 * i) * S::kSlotRow;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
                     __stcg(reinterpret_cast<float2*>(at + wt * CPW + 8 * d + 2 * t), make_float2(o[d][2 * i], o[d][2 * i + 1]));
                 if (t == 0 && wt == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
             }
-            count_in<S, D>(a, cut, st, flags[0], tid);
+            hand_in<S, D>(a, pl, cut, st, flags[0], tid);
         }
     }
 }
@@ -435,44 +435,59 @@ cudaError_t layer_map(CUtensorMap& map, EncodeFn fn, const KvArgs& c, uint16_t* 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Row tiles of a (sequence, head): up to 16 rows go to this file's kernel, two
-// CTAs per SM; more to the other, in equal tiles of up to 128 rows, one CTA per
-// SM.
+// Row tiles of a (sequence, head): up to 16 rows go to this file's kernel, more
+// to the other, in equal tiles of up to 128 rows.  Both run two CTAs per SM.
 struct AttnRows {
-    int row_tiles, tile_rows, ctas;
+    int row_tiles, tile_rows;
 };
 
 AttnRows attn_rows(int m, int group)
 {
     const int rows = m * group;
-    if (rows <= 16) return AttnRows{1, 16, kMaxCtas};
+    if (rows <= 16) return AttnRows{1, 16};
     const int tiles = (rows + 127) / 128;
-    return AttnRows{tiles, (rows + tiles - 1) / tiles, kMaxCtas / 2};
+    return AttnRows{tiles, (rows + tiles - 1) / tiles};
 }
-static_assert(4 * kMaxCtas <= kMaxBlocks);                   // two counters a slot
+static_assert(2 * kMaxCtas + 2 <= kMaxBlocks);               // a counter a slot, and the list's
+
+// Whether the second kernel joins.  It costs a launch, and about 6 us behind
+// the first; one CTA takes 1 to 3 us for the 2 or 3 parts of an ordinary group
+// of 16 rows (32 sequences of up to 4000 tokens: 64 us, with the second kernel
+// 68), but 20 us for 37 parts (one sequence of 131077 tokens: 117 us, 103), and
+// 10 to 17 us for 6 parts of 80 rows (16 drafted tokens of 8 sequences: 63 us,
+// 53).  Short tables are cut into few parts whatever the rows.
+bool defer_join(const KvArgs& c, int n, int tile_rows)
+{
+    const long long tiles = (long long)c.max_pages * c.page_size / kTile + 1;
+    if (tiles / kMinTiles <= kFewParts) return false;
+    return tile_rows > 16 || (long long)n * c.n_heads * kFewParts < kMaxCtas;
+}
 
 template <int D>
-cudaError_t launch_16(const AttnArgs& a, const AttnPlan& pl, int ctas, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                      cudaStream_t stream)
+cudaError_t launch_16(const AttnArgs& a, const AttnPlan& pl, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream)
 {
     using S = Shape16<D>;
     auto kern = paged_attn_kernel<D>;
     static std::atomic<int> done[kMaxDevices];
-    const cudaError_t e = once_per_device(done, [&] {
+    cudaError_t e = once_per_device(done, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)ctas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+    e = launch_pdl(kern, dim3(kMaxCtas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+    return e == cudaSuccess && pl.deferred ? launch_join<S, D>(a, pl, stream) : e;
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim)
 {
-    const AttnRows r = attn_rows(m, n_q_heads / n_heads);
-    const size_t slot = r.ctas < kMaxCtas ? attention_tc_slot_floats(head_dim)
-                                          : head_dim == 128 ? Shape16<128>::kSlot : Shape16<64>::kSlot;
-    return ws_data_off() + align_up(sizeof(float) * 2 * (size_t)r.ctas * slot, 256);
+    if (attn_rows(m, n_q_heads / n_heads).tile_rows > 16) return attention_tc_workspace(head_dim);
+    return head_dim == 128 ? workspace_of<Shape16<128>>() : workspace_of<Shape16<64>>();
+}
+
+int attention_launches(const KvArgs& c, int n, int m, int group)
+{
+    return defer_join(c, n, attn_rows(m, group).tile_rows) ? 2 : 1;
 }
 
 bool attention_tiles_ok(const AttnArgs& a)
@@ -491,11 +506,10 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream)
     CUtensorMap kmap, vmap;
     if ((e = layer_map(kmap, fn, a.c, a.c.k, a.layer)) != cudaSuccess) return e;
     if ((e = layer_map(vmap, fn, a.c, a.c.v, a.layer)) != cudaSuccess) return e;
-    const AttnPlan pl = {r.row_tiles, r.tile_rows, a.n * r.row_tiles, __builtin_ctz(a.c.page_size),
+    const AttnPlan pl = {r.row_tiles, r.tile_rows, a.n * r.row_tiles, __builtin_ctz(a.c.page_size), defer_join(a.c, a.n, r.tile_rows) ? 1 : 0,
                          a.scale * 1.4426950408889634f};
-    if (r.ctas < kMaxCtas) return launch_attention_tc(a, pl, r.ctas, kmap, vmap, stream);
-    return a.c.head_dim == 128 ? launch_16<128>(a, pl, r.ctas, kmap, vmap, stream)
-                               : launch_16<64>(a, pl, r.ctas, kmap, vmap, stream);
+    if (r.tile_rows > 16) return launch_attention_tc(a, pl, kmap, vmap, stream);
+    return a.c.head_dim == 128 ? launch_16<128>(a, pl, kmap, vmap, stream) : launch_16<64>(a, pl, kmap, vmap, stream);
 }
 
 }  // namespace exl3

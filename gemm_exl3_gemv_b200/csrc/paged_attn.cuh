@@ -7,9 +7,9 @@
 // 64-token tiles its rows see (a window skips the tiles in between).  The tiles
 // of all groups, in order, are cut into equal contiguous ranges, one per CTA,
 // so the lengths may be as ragged as they like; the cut is worked out on the
-// device from the lengths.  A group that several CTAs share is joined by the
-// last of them to arrive, in the order of the ranges, in two levels when they
-// are many.  (Ranges that CTAs take as they get done were measured too: the
+// device from the lengths.  A group that several CTAs share is joined in the
+// order of the ranges: by the last CTA to arrive, or, where that would be a lot
+// for one CTA, by a second kernel on the whole GPU (see defer_join()).  (Ranges that CTAs take as they get done were measured too: the
 // equal shares of a 131077-token sequence are done between 66 and 100 us, but
 // each further stretch cost more than the even finish gave.)
 #pragma once
@@ -28,13 +28,14 @@ constexpr int kTile = 64;                                    // tokens per tile
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinTiles = 2;                                 // of a CTA's share, from which another CTA is worth its part of the join
-constexpr int kFan = 8;                                      // parts joined at once
+constexpr int kFewParts = 8;                                 // of a group, which the last CTA to arrive joins
 constexpr int kMaxCtas = 148 * 2;
 
 struct AttnPlan {
     int row_tiles, tile_rows; // row tiles of a (sequence, head), and their rows
     int entries;              // sequences x row tiles
     int page_shift;
+    int deferred;             // parts are joined by the second kernel
     float scale_log2;
 };
 
@@ -288,125 +289,170 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int of, int& flag, in
     return flag;
 }
 
-// Parts of a group, joined by the consumers of one CTA in the order of the
-// parts: written out (last), or to the first part's slot.  A thread takes a
-// float4 of kAcc rows, with kDeep parts in flight (the parts lie in the L2;
-// their latency is the cost), and rescales by the rows' maxima as it goes.
-template <typename S, int D, typename SlotOf>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, const Entry& en, int b, int h, float* slots, int parts,
-                                           SlotOf slot_of, bool last, int tid)
+// A group cut over several CTAs: its parts are in the slots of consecutive
+// ranges' first stretches, but for the first part, which may be its range's
+// last stretch (late).
+struct Pieces {
+    Stretch st;
+    int r_first, parts, late;
+    __device__ __forceinline__ int slot(int c) const { return 2 * (r_first + c) + (c == 0 ? late : 0); }
+};
+__device__ __forceinline__ Pieces pieces_of(const AttnCut& cut, const Stretch& st)
 {
-    constexpr int kVec = D / 4, kStep = S::kConsumers / kVec;    // rows apart
-    constexpr int kAcc = S::kRows / kStep < 4 ? S::kRows / kStep : 4, kDeep = 4;
-    static_assert(S::kRows % (kStep * kAcc) == 0);
-    auto part_of = [&](int c) { return slots + (long long)slot_of(c) * S::kSlot; };
-    const int col = 4 * (tid % kVec);
-    for (int base = 0; base < en.rows; base += kStep * kAcc) {
-        const int r0 = base + tid / kVec;
-        float4 acc[kAcc];
-        float mx[kAcc], sum[kAcc];
+    Pieces g;
+    g.st = st;
+    g.r_first = cut.range_of(st.gstart);
+    g.parts = cut.range_of(st.gstart + st.en.tiles - 1) - g.r_first + 1;
+    g.late = st.gstart == cut.first(g.r_first) ? 0 : 1;
+    return g;
+}
+
+// In the workspace: two counters (groups on the list, CTAs that are done with
+// it) behind the arrival counters, the slots, and the list of cut groups.
+__device__ __forceinline__ uint32_t* list_counters(const AttnArgs& a)
+{
+    return reinterpret_cast<uint32_t*>(a.ws + ws_counter_off()) + kMaxBlocks - 2;
+}
+__device__ __forceinline__ float* slots_of(const AttnArgs& a) { return reinterpret_cast<float*>(a.ws + ws_data_off()); }
+template <typename S>
+__device__ __forceinline__ Pieces* list_of(const AttnArgs& a)
+{
+    return reinterpret_cast<Pieces*>(slots_of(a) + 2ll * kMaxCtas * S::kSlot);
+}
+template <typename S>
+constexpr size_t workspace_of()
+{
+    return ws_data_off() + align_up(sizeof(float) * 2 * kMaxCtas * S::kSlot + sizeof(Pieces) * kMaxCtas, 256);
+}
+
+// Rows base .. of a cut group, joined in the order of the parts and written out
+// by THREADS threads.  A thread takes a float4 of ACC rows, with DEEP parts in
+// flight (the parts lie in the L2; their latency is the cost), and rescales by
+// the rows' maxima as it goes.
+template <typename S, int D, int THREADS, int ACC, int DEEP>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const Pieces& g, int base, int tid)
+{
+    constexpr int kVec = D / 4, kStep = THREADS / kVec;      // rows apart
+    const Entry& en = g.st.en;
+    const float* slots = slots_of(a);
+    const int col = 4 * (tid % kVec), r0 = base + tid / kVec;
+    float4 acc[ACC];
+    float mx[ACC], sum[ACC];
 #pragma unroll
-        for (int i = 0; i < kAcc; ++i) {
-            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            mx[i] = kNegInf;
-            sum[i] = 0.f;
-        }
-        for (int c0 = 0; c0 < parts; c0 += kDeep) {
-            float4 v[kDeep][kAcc];
-            float2 ms[kDeep][kAcc];
+    for (int i = 0; i < ACC; ++i) {
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        mx[i] = kNegInf;
+        sum[i] = 0.f;
+    }
+    for (int c0 = 0; c0 < g.parts; c0 += DEEP) {
+        float4 v[DEEP][ACC];
+        float2 ms[DEEP][ACC];
 #pragma unroll
-            for (int c = 0; c < kDeep; ++c) {
-                const float* from = part_of(c0 + c);
+        for (int c = 0; c < DEEP; ++c) {
+            const float* from = slots + (long long)g.slot(c0 + c) * S::kSlot;
 #pragma unroll
-                for (int i = 0; i < kAcc; ++i) {
-                    const float* at = from + (r0 + i * kStep) * S::kSlotRow;
-                    const bool in = c0 + c < parts;
-                    v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(at + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    ms[c][i] = in ? __ldcg(reinterpret_cast<const float2*>(at + D)) : make_float2(kNegInf, 0.f);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kAcc; ++i) {
-                float now = mx[i];
-#pragma unroll
-                for (int c = 0; c < kDeep; ++c) now = fmaxf(now, ms[c][i].x);
-                const float at = now == kNegInf ? 0.f : now, f0 = ex2(mx[i] - at);
-                mx[i] = now;
-                sum[i] *= f0;
-                acc[i].x *= f0, acc[i].y *= f0, acc[i].z *= f0, acc[i].w *= f0;
-#pragma unroll
-                for (int c = 0; c < kDeep; ++c) {
-                    const float f = ex2(ms[c][i].x - at);
-                    sum[i] += f * ms[c][i].y;
-                    acc[i].x += f * v[c][i].x;
-                    acc[i].y += f * v[c][i].y;
-                    acc[i].z += f * v[c][i].z;
-                    acc[i].w += f * v[c][i].w;
-                }
-            }
-        }
-        // row maxima of the first part are read by other threads until here
-        if (!last) named_bar(1, S::kConsumers);
-#pragma unroll
-        for (int i = 0; i < kAcc; ++i) {
-            const int r = r0 + i * kStep;
-            if (last) {
-                if (r >= en.rows) break;
-                const int rr = en.row0 + r, tok = rr / a.group, head = h * a.group + rr - tok * a.group;
-                const bool none = en.len - en.count + tok < 0;    // a row that sees no token: zeros
-                const float inv = none ? 0.f : 1.f / sum[i];
-                *reinterpret_cast<uint2*>(a.out + b * a.o_bs + tok * a.o_rs + (long long)head * D + col) =
-                    make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
-                if (a.lse && col == 0)
-                    a.lse[((long long)b * a.m + tok) * a.n_q_heads + head] = none ? kNegInf : (mx[i] + (log2f(sum[i]) - S::kUp)) * kLn2;
-            } else {
-                float* at = part_of(0) + r * S::kSlotRow;
-                __stcg(reinterpret_cast<float4*>(at + col), acc[i]);
-                if (col == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
+            for (int i = 0; i < ACC; ++i) {
+                const float* at = from + (r0 + i * kStep) * S::kSlotRow;
+                const bool in = c0 + c < g.parts && r0 + i * kStep < en.rows;
+                v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(at + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                ms[c][i] = in ? __ldcg(reinterpret_cast<const float2*>(at + D)) : make_float2(kNegInf, 0.f);
             }
         }
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) {
+            float now = mx[i];
+#pragma unroll
+            for (int c = 0; c < DEEP; ++c) now = fmaxf(now, ms[c][i].x);
+            const float at = now == kNegInf ? 0.f : now, f0 = ex2(mx[i] - at);
+            mx[i] = now;
+            sum[i] *= f0;
+            acc[i].x *= f0, acc[i].y *= f0, acc[i].z *= f0, acc[i].w *= f0;
+#pragma unroll
+            for (int c = 0; c < DEEP; ++c) {
+                const float f = ex2(ms[c][i].x - at);
+                sum[i] += f * ms[c][i].y;
+                acc[i].x += f * v[c][i].x;
+                acc[i].y += f * v[c][i].y;
+                acc[i].z += f * v[c][i].z;
+                acc[i].w += f * v[c][i].w;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ACC; ++i) {
+        const int r = r0 + i * kStep;
+        if (r >= en.rows) break;
+        const int rr = en.row0 + r, tok = rr / a.group, head = g.st.h * a.group + rr - tok * a.group;
+        const bool none = en.len - en.count + tok < 0;       // a row that sees no token: zeros
+        const float inv = none ? 0.f : 1.f / sum[i];
+        *reinterpret_cast<uint2*>(a.out + g.st.b * a.o_bs + tok * a.o_rs + (long long)head * D + col) =
+            make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
+        if (a.lse && col == 0)
+            a.lse[((long long)g.st.b * a.m + tok) * a.n_q_heads + head] = none ? kNegInf : (mx[i] + (log2f(sum[i]) - S::kUp)) * kLn2;
     }
 }
 
-// Which of a CTA's stretches' slots, and counting in after the partial result
-// is written there: joins what is complete.  Consumer threads.
-template <typename S, int D>
+// Where a stretch's partial result goes.
+template <typename S>
 __device__ __forceinline__ float* slot_at(const AttnArgs& a, const Stretch& st)
 {
-    return reinterpret_cast<float*>(a.ws + ws_data_off()) + (long long)(2 * blockIdx.x + (st.first ? 0 : 1)) * S::kSlot;
+    return slots_of(a) + (long long)(2 * blockIdx.x + (st.first ? 0 : 1)) * S::kSlot;
 }
+// After it is there, the consumer threads: the group of the first part goes on
+// the list for the second kernel, or the last CTA to arrive joins.
 template <typename S, int D>
-__device__ __forceinline__ void count_in(const AttnArgs& a, const AttnCut& cut, const Stretch& st, int& flag, int tid)
+__device__ __forceinline__ void hand_in(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const Stretch& st, int& flag, int tid)
 {
-    float* slots = reinterpret_cast<float*>(a.ws + ws_data_off());
-    uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off());
-    // the group's parts: the first one is its range's first or last stretch, the others first ones
-    const int r_first = cut.range_of(st.gstart), parts = cut.range_of(st.gstart + st.en.tiles - 1) - r_first + 1;
-    const int late = st.gstart == cut.first(r_first) ? 0 : 1;
-    auto slot_of = [&](int c) { return 2 * (r_first + c) + (c == 0 ? late : 0); };
-    // up to kFan parts are joined at once, more in two levels of about the square root
-    int fan = parts;
-    if (parts > kFan)
-        for (fan = kFan / 2; fan * fan < parts; ++fan) {}
-    const int node = ((int)blockIdx.x - r_first) / fan * fan;
-    int from = node, step = 1, count = min(fan, parts - node);
-    uint32_t* counter = counters + slot_of(node);
-    while (last_of(counter, count, flag, tid, S::kConsumers)) {
-        const bool last = step == fan || fan == parts;
-        join_parts<S, D>(a, st.en, st.b, st.h, slots, count, [&](int c) { return slot_of(from + c * step); }, last, tid);
-        if (last) break;
-        from = 0;
-        step = fan;
-        count = (parts + fan - 1) / fan;
-        counter = counters + 2 * kMaxCtas + slot_of(0);
+    const Pieces g = pieces_of(cut, st);
+    if (pl.deferred) {
+        if (tid == 0 && (int)blockIdx.x == g.r_first) list_of<S>(a)[atomicAdd(list_counters(a), 1u)] = g;
+        return;
     }
+    uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + ws_counter_off()) + g.slot(0);
+    if (!last_of(counter, g.parts, flag, tid, S::kConsumers)) return;
+    constexpr int kStep = S::kConsumers / (D / 4), kAcc = S::kRows / kStep < 4 ? S::kRows / kStep : 4;
+    static_assert(S::kRows % (kStep * kAcc) == 0);
+    for (int base = 0; base < st.en.rows; base += kStep * kAcc) join_rows<S, D, S::kConsumers, kAcc, 4>(a, g, base, tid);
+}
+
+// The second kernel: grid (groups that may be cut, rows / kJoinRows).  Few rows
+// come in many parts, many rows in a few.
+constexpr int kJoinThreads = 128;
+template <typename S>
+constexpr int kJoinAcc = S::kRows > 16 ? 2 : 1;
+template <typename S>
+constexpr int kJoinDeep = S::kRows > 16 ? 8 : 16;
+template <typename S, int D>
+constexpr int kJoinRows = kJoinThreads / (D / 4) * kJoinAcc<S>;
+template <typename S, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a)
+{
+    __shared__ Pieces g;
+    grid_dep_wait();
+    grid_dep_launch();
+    uint32_t* counters = list_counters(a);
+    const bool in = blockIdx.x < *reinterpret_cast<volatile uint32_t*>(counters);
+    const int* from = reinterpret_cast<const int*>(list_of<S>(a) + blockIdx.x);    // read before it is known whether there is one
+    for (int i = threadIdx.x; i < (int)(sizeof(Pieces) / 4); i += kJoinThreads) reinterpret_cast<int*>(&g)[i] = __ldcg(from + i);
+    __syncthreads();
+    const int base = blockIdx.y * kJoinRows<S, D>;
+    if (in && base < g.st.en.rows) join_rows<S, D, kJoinThreads, kJoinAcc<S>, kJoinDeep<S>>(a, g, base, threadIdx.x);
+    if (threadIdx.x == 0 && atomicAdd(counters + 1, 1u) == gridDim.x * gridDim.y - 1) counters[0] = counters[1] = 0;
+}
+
+template <typename S, int D>
+cudaError_t launch_join(const AttnArgs& a, const AttnPlan& pl, cudaStream_t stream)
+{
+    const long long groups = (long long)pl.entries * a.c.n_heads;
+    const dim3 grid((unsigned)(groups < kMaxCtas ? groups : kMaxCtas), (unsigned)((pl.tile_rows + kJoinRows<S, D> - 1) / kJoinRows<S, D>));
+    return launch_pdl(join_kernel<S, D>, grid, dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace attn
 
 // The launch of the kernel for more than 16 rows (paged_attn_tc.cu).
-cudaError_t launch_attention_tc(const AttnArgs& a, const attn::AttnPlan& pl, int ctas, const CUtensorMap& kmap,
+cudaError_t launch_attention_tc(const AttnArgs& a, const attn::AttnPlan& pl, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, cudaStream_t stream);
-size_t attention_tc_slot_floats(int head_dim);
+size_t attention_tc_workspace(int head_dim);
 
 }  // namespace exl3

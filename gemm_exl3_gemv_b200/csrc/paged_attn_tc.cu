@@ -37,11 +37,11 @@ struct ShapeTc {
     static constexpr int kRows = 128;
     static constexpr int kHalf = kTile * D * 2;              // bytes of a tile's keys (or values)
     static constexpr int kQ = kRows * D * 2;
-    static constexpr int kP = kRows * kTile * 2;             // of one tile; two in turn
-    static constexpr int kFronts = (kThreads + kThreads / 32 + 3) / 4 * 16;
-    static constexpr int kRest = kQ + 2 * kP + kFronts + 512;
-    static constexpr int kStages = (227 * 1024 - kRest) / (2 * kHalf) < 8 ? (227 * 1024 - kRest) / (2 * kHalf) : 8;
+    static constexpr int kP = kRows * kTile * 2;             // of one tile
+    static constexpr int kRest = kQ + kP + 512;
+    static constexpr int kStages = (113 * 1024 - kRest) / (2 * kHalf);           // two CTAs per SM
     static constexpr int kSmem = kStages * 2 * kHalf + kRest;
+    static_assert((kThreads + kThreads / 32) * 4 <= kP);     // the fronts lie there until the producer has read them
     static constexpr int kTmemCols = 256;                    // O: D columns from 128 on; S: 64 columns at 0 and at 64
     static constexpr int kSlotRow = D + 4;                   // a row of a partial result: D sums, maximum, sum
     static constexpr int kSlot = kRows * kSlotRow;
@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t swizzled(int rows, int row, int chunk)
 }
 
 template <int D>
-__global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
+__global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
     paged_attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan pl,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
@@ -104,23 +104,23 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];          // the swizzle counts rows from 1024-byte borders
     unsigned char* q_smem = smem + S::kStages * 2 * S::kHalf;
     unsigned char* p_smem = q_smem + S::kQ;
-    int* front = reinterpret_cast<int*>(p_smem + 2 * S::kP);
-    uint64_t* full = reinterpret_cast<uint64_t*>(front + S::kFronts / 4);
+    int* front = reinterpret_cast<int*>(p_smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(p_smem + S::kP);
     uint64_t* empty = full + S::kStages;
     uint64_t* told = empty + S::kStages;
     uint64_t* heard = told + 2;
     uint64_t* s_full = heard + 2;                            // scores of a buffer are there, are read
     uint64_t* s_free = s_full + 2;
-    uint64_t* p_full = s_free + 2;                           // probabilities of a buffer are there, their product is done
-    uint64_t* pv_done = p_full + 2;
-    uint64_t* q_full = pv_done + 2;
+    uint64_t* p_full = s_free + 2;                           // a tile's probabilities are there, their product is done
+    uint64_t* pv_done = p_full + 1;
+    uint64_t* q_full = pv_done + 1;
     uint64_t* all_done = q_full + 1;
     Stretch* notes = reinterpret_cast<Stretch*>(all_done + 1);
     // last to arrive; a wait of the softmax warps has run out; tile that holds values that are not finite (by parity);
     // tile whose stretch's O begins with them
     int* flags = reinterpret_cast<int*>(notes + 2);
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(flags + 5);
-    static_assert((2 * S::kStages + 14) * 8 + 2 * sizeof(Stretch) + 24 <= 512);
+    static_assert((2 * S::kStages + 12) * 8 + 2 * sizeof(Stretch) + 24 <= 512);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
             mbar_init(heard + i, 5);
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
-            mbar_init(p_full + i, 4);
-            mbar_init(pv_done + i, 1);
         }
+        mbar_init(p_full, 4);
+        mbar_init(pv_done, 1);
         mbar_init(q_full, 4);
         mbar_init(all_done, 1);
         fence_mbar_init();
@@ -168,24 +168,24 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
         constexpr uint32_t id_qk = idesc_f16(128, kTile, false), id_pv = idesc_f16(128, D, true);
         const uint32_t q_at = smem_u32(q_smem);
         Turn<S::kStages> next, done;                         // tiles whose scores, whose results were asked for
-        Turn<2> note, s_buf, p_buf;
-        uint32_t q_phase = 0;
+        Turn<2> note, s_buf;
+        uint32_t q_phase = 0, p_phase = 0;
         int tile = 0;                                        // of this CTA
         auto result = [&](bool first) {                      // O (+)= P V of the oldest tile without it
-            p.wait(p_full + p_buf.at, p_buf.phase);
+            p.wait(p_full, p_phase);
+            p_phase ^= 1;
             if (p.alive) {
                 tc_fence_after();
-                const uint32_t pt = smem_u32(p_smem) + p_buf.at * S::kP, vt = smem_u32(smem + done.at * 2 * S::kHalf) + S::kHalf;
+                const uint32_t pt = smem_u32(p_smem), vt = smem_u32(smem + done.at * 2 * S::kHalf) + S::kHalf;
                 const bool fresh = first && *reinterpret_cast<volatile int*>(flags + 4) != tile;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
                     mma_f16_ss_elect(tmem_o, sdesc_sw128(pt + 32 * k, 16, 1024), sdesc_sw128(vt + 2048 * k, kTile * 128, 1024),
                                      id_pv, fresh && k == 0 ? 0u : 1u);
                 mma_commit_elect(empty + done.at);
-                mma_commit_elect(pv_done + p_buf.at);
+                mma_commit_elect(pv_done);
             }
             done.next();
-            p_buf.next();
         };
         while (p.alive) {
             p.wait(told + note.at, note.phase);
@@ -227,12 +227,11 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         const auto everyone = [] { named_bar(1, S::kConsumers); };
         Turn<S::kStages> stage;
-        Turn<2> note, s_buf, p_buf, pv;                      // pv: the oldest tile whose product was not waited for
+        Turn<2> note, s_buf;
         int tile = 0, waited = 0;                            // of this CTA
         auto wait_products = [&](int upto) {                 // of the CTA's first `upto` tiles
             for (; waited < upto; ++waited) {
-                p.wait(pv_done + pv.at, pv.phase);
-                pv.next();
+                p.wait(pv_done, waited & 1);
             }
             tc_fence_after();
         };
@@ -284,9 +283,14 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free + s_buf.at);
                 s_buf.next();
-                float s[kTile];
+                float s[kTile], scale = pl.scale_log2;       // positive from here on: scores are scaled behind their maximum
 #pragma unroll
-                for (int j = 0; j < kTile; ++j) s[j] = __uint_as_float(bits[j]) * pl.scale_log2;
+                for (int j = 0; j < kTile; ++j) s[j] = __uint_as_float(bits[j]);
+                if (!(scale > 0.f)) {
+#pragma unroll
+                    for (int j = 0; j < kTile; ++j) s[j] *= scale;
+                    scale = 1.f;
+                }
                 const uint32_t vt = smem_u32(smem + stage.at * 2 * S::kHalf) + S::kHalf;
                 const bool whole = tok0 + kTile <= all_hi && (tok0 >= all_lo || tok0 + kTile <= a.sinks);
                 bool odd_values = false;
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                     for (int j = 0; j < kTile; ++j) s[j] = j < hi && (j >= lo || j < sk) ? s[j] : kNegInf;
                     // values: what no row of the tile sees is cleared; is there anything that is not finite?
                     p.wait(full + stage.at, stage.phase);
-                    wait_products(tile - 1);                 // every warp has read the word of two tiles ago
+                    wait_products(tile - 1);                 // every warp has read the flag of two tiles ago
                     bool odd = false;
 #pragma unroll 2
                     for (int i = tid; i < kTile * (D / 8); i += S::kConsumers) {
@@ -313,9 +317,10 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                 }
                 stage.next();
 
-                float top = s[0];
+                float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int j = 1; j < kTile; ++j) top = fmaxf(top, s[j]);
+                for (int j = 4; j < kTile; ++j) tops[j & 3] = fmaxf(tops[j & 3], s[j]);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
                 // the first tile sets the row's maximum; later ones where it has grown too much
                 const bool grown = top > mx + S::kGap || mx == kNegInf;
                 const float now = grown ? top : mx, cut_at = now == kNegInf ? 0.f : now;
@@ -341,13 +346,13 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                 float part[4] = {};
 #pragma unroll
                 for (int j = 0; j < kTile; ++j) {
-                    s[j] = ex2(s[j] + shift);
+                    s[j] = ex2(fmaf(s[j], scale, shift));
                     part[j & 3] += s[j];
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
-                // to the operand's place, once the product two tiles ago has read it
-                wait_products(tile - 1);
-                const uint32_t pt = smem_u32(p_smem) + p_buf.at * S::kP;
+                // to the operand's place, once the last product has read it
+                wait_products(tile);
+                const uint32_t pt = smem_u32(p_smem);
 #pragma unroll
                 for (int c = 0; c < kTile / 8; ++c)
                     sts16(pt + swizzled(S::kRows, row, c), make_uint4(pack2(s[8 * c], s[8 * c + 1]), pack2(s[8 * c + 2], s[8 * c + 3]),
@@ -355,7 +360,6 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                 if (odd_values) {
                     // values that are not finite go to the rows that see them here, and are cleared for the product;
                     // a stretch's first tile then adds to an O that begins with them
-                    wait_products(tile);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
@@ -400,15 +404,14 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                 fence_proxy_async_smem();                    // probabilities and cleared values, for the tensor cores
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + p_buf.at);
-                p_buf.next();
+                if (lane == 0) mbar_arrive(p_full);
             }
 
             // ---- the stretch's result ----
             wait_products(first_tile + st.n);
             const bool complete = st.n == en.tiles;
             const float inv = pos < 0 ? 0.f : 1.f / sum;     // a row that sees no token: zeros
-            float* slot = slot_at<S, D>(a, st) + row * S::kSlotRow;
+            float* slot = slot_at<S>(a, st) + row * S::kSlotRow;
             uint16_t* out = a.out + st.b * a.o_bs + tok * a.o_rs + (long long)head * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
                     a.lse[((long long)st.b * a.m + tok) * a.n_q_heads + head] = pos < 0 ? kNegInf : (mx + (log2f(sum) - S::kUp)) * kLn2;
             } else {
                 if (mine) __stcg(reinterpret_cast<float2*>(slot + D), make_float2(mx, sum));
-                count_in<S, D>(a, cut, st, flags[0], tid);
+                hand_in<S, D>(a, pl, cut, st, flags[0], tid);
             }
         }
     }
@@ -451,27 +454,30 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_tc(const AttnArgs& a, const AttnPlan& pl, int ctas, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                      cudaStream_t stream)
+cudaError_t launch_tc(const AttnArgs& a, const AttnPlan& pl, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream)
 {
     using S = ShapeTc<D>;
     auto kern = paged_attn_tc_kernel<D>;
     static std::atomic<int> done[kMaxDevices];
-    const cudaError_t e = once_per_device(done, [&] {
+    cudaError_t e = once_per_device(done, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)ctas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+    e = launch_pdl(kern, dim3(kMaxCtas), dim3(S::kThreads), S::kSmem, stream, a, pl, kmap, vmap);
+    return e == cudaSuccess && pl.deferred ? launch_join<S, D>(a, pl, stream) : e;
 }
 
 }  // namespace
 
-size_t attention_tc_slot_floats(int head_dim) { return head_dim == 128 ? ShapeTc<128>::kSlot : ShapeTc<64>::kSlot; }
-
-cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& pl, int ctas, const CUtensorMap& kmap,
-                                const CUtensorMap& vmap, cudaStream_t stream)
+size_t attention_tc_workspace(int head_dim)
 {
-    return a.c.head_dim == 128 ? launch_tc<128>(a, pl, ctas, kmap, vmap, stream) : launch_tc<64>(a, pl, ctas, kmap, vmap, stream);
+    return head_dim == 128 ? workspace_of<ShapeTc<128>>() : workspace_of<ShapeTc<64>>();
+}
+
+cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& pl, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                cudaStream_t stream)
+{
+    return a.c.head_dim == 128 ? launch_tc<128>(a, pl, kmap, vmap, stream) : launch_tc<64>(a, pl, kmap, vmap, stream);
 }
 
 }  // namespace exl3

@@ -37,7 +37,8 @@ EXPORTS = ("exl3_status_string", "exl3_last_cuda_error", "exl3_version", "exl3_w
            "exl3_gemv_noalloc", "exl3_grouped_workspace_bytes", "exl3_gemm_grouped", "exl3_q4_workspace_bytes",
            "exl3_q4_gemm", "exl3_q4_pack", "exl3_kv_scratch_bytes", "exl3_kv_reset", "exl3_kv_status",
            "exl3_kv_extend", "exl3_kv_write", "exl3_kv_truncate", "exl3_kv_fork", "exl3_kv_compact",
-           "exl3_paged_attention_workspace_bytes", "exl3_paged_attention")
+           "exl3_paged_attention_workspace_bytes", "exl3_paged_attention_launches",
+           "exl3_paged_attention")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libexl3.so not built ({LIB_PATH}); run `python -m gemm_exl3_gemv_b200.build`")
@@ -124,6 +125,8 @@ lib.exl3_paged_attention.argtypes = [_P, _I, _I, _I, _P, _P, _P, _L, _L, _I, _F,
 for _name in ("reset", "status", "extend", "write", "truncate", "fork", "compact"):
     getattr(lib, "exl3_kv_" + _name).restype = _I
 lib.exl3_paged_attention.restype = _I
+lib.exl3_paged_attention_launches.argtypes = [_P, _I, _I, _I]
+lib.exl3_paged_attention_launches.restype = _I
 
 
 class Exl3Error(RuntimeError):

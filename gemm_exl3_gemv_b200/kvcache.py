@@ -193,6 +193,10 @@ class KvCache:
             raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"attention of {m} rows with {n_q_heads} heads")
         return torch.zeros(max(need), dtype=torch.uint8, device=self.device)
 
+    def attention_launches(self, n: int, m: int, n_q_heads: int) -> int:
+        """Kernel launches of one attention call of this size."""
+        return int(ex.lib.exl3_paged_attention_launches(self._ref, n, m, n_q_heads))
+
     def attention(self, layer: int, seqs: torch.Tensor, q: torch.Tensor, counts: Optional[torch.Tensor] = None,
                   scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:

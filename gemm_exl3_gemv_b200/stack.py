@@ -232,7 +232,7 @@ class Stack:
             else:
                 total += ex.grouped_kernel_launches(m)
         if self.cache is not None:                      # truncate and extend; write and attention per layer
-            total += 2 + 2 * len(self.layers)
+            total += 2 + (1 + self.cache.attention_launches(1, m, self.q_heads)) * len(self.layers)
         return total
 
     # -------------------------------------------------------------- run ---

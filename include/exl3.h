@@ -479,6 +479,8 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  * exl3_gemm_small_m (exl3_workspace_status).
  */
 EXL3_API size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
+/* Kernel launches of one call (0 for an invalid one).  Host-only. */
+EXL3_API int exl3_paged_attention_launches(const exl3_kv_cache_t *cache, int n, int m, int n_q_heads);
 EXL3_API int exl3_paged_attention(const exl3_kv_cache_t *cache, int layer, int n, int m, const int32_t *seqs,
                                   const int32_t *counts, const uint16_t *q, long long q_batch_stride,
                                   long long q_row_stride, int n_q_heads, float scale, int window, int sinks,
