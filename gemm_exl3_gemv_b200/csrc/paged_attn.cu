@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
 
     const int total = count_tiles<S::kThreads>(a, pl, front, front + S::kThreads);
     if (total == 0) return;
-    const AttnCut cut(total, gridDim.x);
+    const AttnCut cut(total, gridDim.x, pl.least);
     if ((int)blockIdx.x >= cut.ranges) return;
 
     Patience p = {reinterpret_cast<uint32_t*>(a.ws), true};
@@ -450,6 +450,8 @@ AttnRows attn_rows(int m, int group)
 }
 static_assert(2 * kMaxCtas + 2 <= kMaxBlocks);               // a counter a slot, and the list's
 
+constexpr int kLeastTiles = 2;                               // of a CTA's share, without the second kernel
+
 // Whether the second kernel joins.  It costs a launch, and about 6 us behind
 // the first; one CTA takes 1 to 3 us for the 2 or 3 parts of an ordinary group
 // of 16 rows (32 sequences of up to 4000 tokens: 64 us, with the second kernel
@@ -459,7 +461,7 @@ static_assert(2 * kMaxCtas + 2 <= kMaxBlocks);               // a counter a slot
 bool defer_join(const KvArgs& c, int n, int tile_rows)
 {
     const long long tiles = (long long)c.max_pages * c.page_size / kTile + 1;
-    if (tiles / kMinTiles <= kFewParts) return false;
+    if (tiles / kLeastTiles <= kFewParts) return false;
     return tile_rows > 16 || (long long)n * c.n_heads * kFewParts < kMaxCtas;
 }
 
@@ -506,7 +508,13 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream)
     CUtensorMap kmap, vmap;
     if ((e = layer_map(kmap, fn, a.c, a.c.k, a.layer)) != cudaSuccess) return e;
     if ((e = layer_map(vmap, fn, a.c, a.c.v, a.layer)) != cudaSuccess) return e;
-    const AttnPlan pl = {r.row_tiles, r.tile_rows, a.n * r.row_tiles, __builtin_ctz(a.c.page_size), defer_join(a.c, a.n, r.tile_rows) ? 1 : 0,
+    // Another CTA for fewer tiles than these costs more in the join than it
+    // saves: one sequence of 8192 tokens takes 20, 17.5 and 18.3 us with 2, 4
+    // and 8, 16 drafted tokens behind it 41, 35 and 32 us; without the second
+    // kernel, one of 100 tokens takes 7, 10 and 16 us.
+    const bool deferred = defer_join(a.c, a.n, r.tile_rows);
+    const int least = !deferred ? kLeastTiles : r.tile_rows > 16 ? 8 : 4;
+    const AttnPlan pl = {r.row_tiles, r.tile_rows, a.n * r.row_tiles, __builtin_ctz(a.c.page_size), deferred, least,
                          a.scale * 1.4426950408889634f};
     if (r.tile_rows > 16) return launch_attention_tc(a, pl, kmap, vmap, stream);
     return a.c.head_dim == 128 ? launch_16<128>(a, pl, kmap, vmap, stream) : launch_16<64>(a, pl, kmap, vmap, stream);

@@ -27,7 +27,6 @@ namespace attn {
 constexpr int kTile = 64;                                    // tokens per tile
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinTiles = 2;                                 // of a CTA's share, from which another CTA is worth its part of the join
 constexpr int kFewParts = 8;                                 // of a group, which the last CTA to arrive joins
 constexpr int kMaxCtas = 148 * 2;
 
@@ -36,6 +35,7 @@ struct AttnPlan {
     int entries;              // sequences x row tiles
     int page_shift;
     int deferred;             // parts are joined by the second kernel
+    int least;                // tiles of a CTA's share
     float scale_log2;
 };
 
@@ -43,9 +43,9 @@ struct AttnPlan {
 // more than `share`.
 struct AttnCut {
     int ranges, share, more;
-    __device__ __forceinline__ AttnCut(int total, int ctas)
+    __device__ __forceinline__ AttnCut(int total, int ctas, int least)
     {
-        ranges = min(ctas, (total + kMinTiles - 1) / kMinTiles);
+        ranges = min(ctas, (total + least - 1) / least);
         share = total / ranges;
         more = total - share * ranges;
     }

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
     grid_dep_launch();
     const int total = count_tiles<S::kThreads>(a, pl, front, front + S::kThreads);
     if (total == 0) return;
-    const AttnCut cut(total, gridDim.x);
+    const AttnCut cut(total, gridDim.x, pl.least);
     if ((int)blockIdx.x >= cut.ranges) return;
     if (warp == 5) {
         tmem_alloc(tmem_base, S::kTmemCols);
