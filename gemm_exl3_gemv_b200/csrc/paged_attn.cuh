@@ -200,6 +200,8 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
     const int lane = threadIdx.x & 31, heads = a.c.n_heads, per = (pl.entries + THREADS - 1) / THREADS;
     Turn<STAGES> stage;
     Turn<2> note;
+    // a nonzero injection word (tests of the timeout path) withholds every copy
+    p.alive = *reinterpret_cast<const volatile uint32_t*>(a.ws + kWsInjectOff) == 0u;
     int u = cut.first(blockIdx.x);
     const int u1 = cut.first(blockIdx.x + 1);
     // the entry that tile u belongs to: of the last thread whose entries begin at or in front of it

@@ -476,7 +476,9 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  * A table entry out of range is not followed: exl3_kv_status then reports
  * EXL3_ERR_INDEX, and the rows that needed it are not valid; the same for a
  * bad number in seqs, whose rows are left as they were.  Bounded waits as in
- * exl3_gemm_small_m (exl3_workspace_status).
+ * exl3_gemm_small_m (exl3_workspace_status; its injection word withholds every
+ * copy here too).  After EXL3_ERR_TIMEOUT, zero-fill the workspace before its
+ * next use: parts of a cut sequence may have been counted and not joined.
  */
 EXL3_API size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
 /* Kernel launches of one call (0 for an invalid one).  Host-only. */

@@ -137,6 +137,15 @@ def test_q4(ex):
     assert g(P(16), 64, 16, P(24), None) == ex.EXL3_ERR_MISALIGNED
 
 
+def test_attention_launches(ex):
+    f = ex.lib.exl3_paged_attention_launches
+    c = cache(ex)                                       # 16 pages of 32: eight tiles of 64 tokens
+    assert f(c, 1, 1, 8) == f(c, 1, 32, 8) == 1
+    c = cache(ex, max_pages=4096)
+    assert f(c, 1, 1, 8) == f(c, 1, 32, 8) == f(c, 500, 32, 8) == 2 and f(c, 500, 1, 8) == 1
+    assert f(c, 0, 1, 8) == f(c, 1025, 1, 8) == f(c, 1, 0, 8) == f(c, 1, 33, 8) == f(c, 1, 1, 6) == f(cache(ex, k=None), 1, 1, 8) == 0
+
+
 def test_status_strings(ex):
     assert b"CACHE_FULL" in ex.lib.exl3_status_string(ex.EXL3_ERR_CACHE_FULL)
     assert b"INDEX" in ex.lib.exl3_status_string(ex.EXL3_ERR_INDEX)

@@ -127,13 +127,14 @@ def test_large_scores_and_other_scales(ex):
         c.check(c.run(scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("group", [2, 3])                    # 12 and 18 rows: both kernels
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), 65504.0])
-def test_unseen_tokens_do_not_matter(ex, value):
+def test_unseen_tokens_do_not_matter(ex, value, group):
     """Keys and values that are not finite, in tokens that a row does not see: later drafted tokens, tokens
     outside the window.  The rows that do see one get what the formula gives (not a finite number)."""
     import torch
     m, window, sinks = 6, 40, 2
-    c = Case([100, 170], [m, m], dim=64, page=32, m=m, group=3, seed=8)
+    c = Case([100, 170], [m, m], dim=64, page=32, m=m, group=group, seed=8)
     seen_by = {}
     for s, n in enumerate(c.lens):
         for t in (n - 2, n - m, 3, n - m - window):          # late draft, first draft, never seen, just out of the first row
@@ -160,10 +161,11 @@ def test_unseen_tokens_do_not_matter(ex, value):
             assert np.all(np.abs(out[s, i] - ref[0])[:, cols] <= tol[0][:, cols]), (s, i)
 
 
-def test_unseen_keys_do_not_matter(ex):
+@pytest.mark.parametrize("dim,group", [(64, 3), (64, 8), (128, 4), (128, 32)])
+def test_unseen_keys_do_not_matter(ex, dim, group):
     import torch
     m = 4
-    c = Case([90, 130], [m, m], dim=64, page=32, m=m, group=3, seed=9)
+    c = Case([90, 130], [m, m], dim=dim, page=32, m=m, group=group, seed=9)
     first = c.run()[0].clone()
     for s, n in enumerate(c.lens):
         t = n - 1                                            # seen by the last row alone
@@ -328,3 +330,53 @@ def test_refusals(ex):
         with pytest.raises(ex.Exl3Error) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("m,group", [(1, 4), (12, 4)])                  # both kernels
+def test_withheld_tiles_time_out_and_report(ex, m, group):
+    """Every copy withheld through the workspace's injection word: the waits run out, the call ends and the
+    status says so; with the workspace cleared the next call is right."""
+    c = Case([3000, 70, 400], [m, m, m], dim=128, page=64, m=m, group=group, seed=18)
+    ws = c.cache.attention_workspace(3, m, 2 * group)
+    ws[4:8] = 1
+    c.run(workspace=ws)
+    assert ex.workspace_status(ws) == ex.EXL3_ERR_TIMEOUT
+    ws.zero_()
+    c.check(c.run(workspace=ws))
+    assert ex.workspace_status(ws) == ex.EXL3_OK
+
+
+def test_launch_counts(ex):
+    """One kernel where the table is short, or the parts of a sequence are few; two otherwise."""
+    c = Case([70, 90], [1, 1], kv_heads=2, group=4, dim=64)
+    assert c.cache.attention_launches(2, 1, 8) == 1 == c.cache.attention_launches(2, 32, 8)
+    d = Case([2000], [1], kv_heads=2, group=4, dim=64, page=64)
+    assert d.cache.attention_launches(1, 1, 8) == 2 == d.cache.attention_launches(900, 32, 8)
+    assert d.cache.attention_launches(1000, 1, 8) == 1
+    assert d.cache.attention_launches(0, 1, 8) == d.cache.attention_launches(1, 33, 8) == d.cache.attention_launches(1, 1, 7) == 0
+
+
+@pytest.mark.parametrize("m,group", [(1, 5), (3, 5), (5, 7), (16, 5), (32, 8)])
+def test_joined_by_the_second_kernel(ex, m, group):
+    """Few long sequences, cut into many parts: 16 rows and more, one row tile and several."""
+    for heads, dim, lens in ((1, 64, [9000]), (2, 128, [5000, 300, 1200])):
+        c = Case(lens, [m] + [max(1, m - 1)] * (len(lens) - 1), kv_heads=heads, group=group, dim=dim, page=64, m=m, seed=m + dim)
+        assert c.cache.attention_launches(len(lens), m, heads * group) == 2
+        c.check(c.run())
+
+
+def test_two_streams_with_their_own_workspaces(ex):
+    """Two calls on one cache at once: reads only, each with its workspace."""
+    import torch
+    c = Case([5000, 900], [1, 1], dim=128, page=64, group=4, seed=19)
+    q, seqs = torch.from_numpy(c.q).cuda(), c.ids(c.seqs)
+    want = c.cache.attention(0, seqs, q)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [c.cache.attention_workspace(2, 1, 8) for _ in streams]
+    outs = [torch.empty_like(want) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws, o in zip(streams, spaces, outs):
+            c.cache.attention(0, seqs, q, out=o, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
