@@ -38,9 +38,8 @@ constexpr int kKvFault = 0;           // word: kKvFull | kKvIndex
 constexpr int kKvArrived = 1;         // word: CTAs of an extend that are done
 constexpr int kKvMoves = 2;           // word: pages a compaction moves
 constexpr int kKvUsed = 3;            // word: used pages
-constexpr int kKvCopy = 64;           // kKvMaxList words: pages that copies of shared pages go to
-constexpr int kKvMaxList = 1024;
-constexpr int kKvLists = kKvCopy + kKvMaxList;   // n_pages words: sources, then destinations, of moves; then the new ids
+constexpr int kKvLists = 64;          // n_pages words: sources, then destinations, of moves
+constexpr int kKvMaxList = 1024;      // entries of a list of sequences
 constexpr int kKvFull = 1, kKvIndex = 2;
 
 struct KvArgs {
@@ -56,7 +55,7 @@ struct KvArgs {
 
 inline size_t kv_scratch_bytes(int n_pages)
 {
-    return sizeof(int) * ((size_t)kKvLists + 2 * (size_t)((n_pages + 63) / 64 * 64));
+    return sizeof(int) * ((size_t)kKvLists + (size_t)((n_pages + 63) / 64 * 64));
 }
 cudaError_t launch_kv_reset(const KvArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_extend(const KvArgs& a, int n, int m, const int* seqs, const int* counts, cudaStream_t stream);

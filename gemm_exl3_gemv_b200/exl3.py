@@ -151,6 +151,8 @@ def _ptr(t: Optional[torch.Tensor]):
 # instead of 3.3 us, of a small call's 10.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+# the same for the current device (CUDA is initialised: there is a tensor on a GPU)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream=None):
@@ -309,6 +311,9 @@ def gemm_grouped(problems, bits: int, fp32: bool = False, workspace: Optional[to
 
 # ------------------------------------------------- plain 4-bit weights ---
 
+_F16, _I32, _U8 = torch.float16, torch.int32, torch.uint8
+
+
 def _dense(t: torch.Tensor, dtype, shape, device: int) -> bool:
     """Whether t is a contiguous tensor of this type and shape on that GPU."""
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device
@@ -328,7 +333,7 @@ def _room(ws: torch.Tensor, device: int) -> int:
     """Bytes of a workspace tensor."""
     if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on cuda:{device}")
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def q4_workspace_bytes(m: int, k_in: int, n_out: int) -> int:
@@ -368,7 +373,7 @@ def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Op
     squeeze = x.dim() == 1
     x2 = x.reshape(1, -1) if squeeze else x
     device = x.get_device()
-    if x2.dim() != 2 or packed.dim() != 4 or device < 0 or device != torch.cuda.current_device():
+    if x2.dim() != 2 or packed.dim() != 4 or device < 0 or device != _current_device():
         raise ValueError("expected x of (m, k_in) or (k_in,) on the current CUDA device and packed of "
                          "(n_out/16, k_in/64, 32, 4)")
     (m, k_in), tiles = x2.shape, packed.shape[0]
@@ -377,10 +382,11 @@ def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Op
         raise Exl3Error(EXL3_ERR_UNSUPPORTED, f"q4_gemm of {m} rows, k_in {k_in}, group {group}")
     groups = (k_in // group, n_out)
     # one condition on the usual path: a call of a small product is bound by the host
-    if not (x2.dtype is torch.float16 and x2.is_contiguous() and packed.dtype is torch.int32 and
-            packed.shape == (tiles, k_in // 64, 32, 4) and packed.is_contiguous() and packed.get_device() == device and
-            scale.dtype is torch.float16 and scale.shape == groups and scale.is_contiguous() and
-            scale.get_device() == device and (zero is None or _dense(zero, torch.uint8, groups, device))):
+    if not (x2.dtype is _F16 and packed.dtype is _I32 and scale.dtype is _F16 and x2.is_contiguous() and
+            packed.is_contiguous() and scale.is_contiguous() and packed.shape == (tiles, k_in // 64, 32, 4) and
+            scale.shape == groups and packed.get_device() == device and scale.get_device() == device and
+            (zero is None or zero.dtype is _U8 and zero.shape == groups and zero.is_contiguous() and
+             zero.get_device() == device)):
         _expect(x2, "x", torch.float16, (m, k_in), device)
         _expect(packed, "packed", torch.int32, (tiles, k_in // 64, 32, 4), device)
         _expect(scale, "scale", torch.float16, groups, device)

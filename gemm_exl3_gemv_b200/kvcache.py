@@ -33,6 +33,10 @@ from . import exl3 as ex
 MAX_LIST = 1024         # entries of a list of sequences
 MAX_ROWS = 32           # new tokens per sequence of one attention call
 
+_F16, _I32 = torch.float16, torch.int32
+_extend, _write, _truncate = ex.lib.exl3_kv_extend, ex.lib.exl3_kv_write, ex.lib.exl3_kv_truncate
+_fork, _compact, _attention = ex.lib.exl3_kv_fork, ex.lib.exl3_kv_compact, ex.lib.exl3_paged_attention
+
 
 class KvCache:
     """k, v: (n_layers, n_pages, n_heads, page_size, head_dim) fp16; table:
@@ -80,26 +84,27 @@ class KvCache:
         return cache
 
     # ------------------------------------------------------------ checks ---
+    # Small calls are bound by the host, so each check is one condition on its
+    # usual path.
 
-    def _list(self, t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[int]:
-        """Checks a list of int32 numbers (of n entries); its address, None for
-        no list."""
+    def _list(self, t: Optional[torch.Tensor], what: str, n: int) -> Optional[int]:
+        """Checks a list of n int32 numbers; its address, None for no list."""
         if t is None:
             return None
-        if t.dim() != 1 or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != self._index:
+        if t.dtype is _I32 and t.shape == (n,) and n <= MAX_LIST and t.is_contiguous() and t.get_device() == self._index:
+            return t.data_ptr()
+        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{what}: expected a contiguous one-dimensional int32 tensor on {self.device}, got {t.dtype} "
                              f"of shape {tuple(t.shape)} on {t.device}")
-        if n is not None and t.shape[0] != n:
+        if t.shape[0] != n:
             raise ValueError(f"{what}: expected {n} entries, got {t.shape[0]}")
-        if t.shape[0] > MAX_LIST:
-            raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"{what}: a list of more than {MAX_LIST} entries")
-        return t.data_ptr()
+        raise ex.Exl3Error(ex.EXL3_ERR_UNSUPPORTED, f"{what}: a list of more than {MAX_LIST} entries")
 
     def _rows(self, t: torch.Tensor, what: str, n: int, heads: int):
         """Checks (n, m, heads, head_dim) rows, dense within a row; returns m and
         the strides between entries and between rows."""
         shape = t.shape
-        if len(shape) != 4 or t.dtype is not torch.float16 or shape[0] != n or shape[2] != heads or \
+        if len(shape) != 4 or t.dtype is not _F16 or shape[0] != n or shape[2] != heads or \
                 shape[3] != self.head_dim or t.get_device() != self._index:
             raise ValueError(f"{what}: expected fp16 of shape ({n}, m, {heads}, {self.head_dim}) on {self.device}, got "
                              f"{t.dtype} {tuple(shape)} on {t.device}")
@@ -120,9 +125,15 @@ class KvCache:
 
     def _where(self, stream):
         """The stream's handle; the cache's device must be the current one."""
-        if torch.cuda.current_device() != self._index:
+        if ex._current_device() != self._index:
             raise ValueError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
         return ex._raw_stream(self._index) if stream is None else stream.cuda_stream
+
+    @staticmethod
+    def _entries(t: torch.Tensor, what: str) -> int:
+        if t.dim() != 1:
+            raise ValueError(f"{what}: expected a one-dimensional tensor, got shape {tuple(t.shape)}")
+        return t.shape[0]
 
     # ------------------------------------------------------- bookkeeping ---
 
@@ -143,42 +154,51 @@ class KvCache:
     def extend(self, seqs: torch.Tensor, m: int, counts: Optional[torch.Tensor] = None, stream=None):
         """Each sequence of ``seqs`` grows by ``m`` tokens (counts: by
         counts[b], 0..m), whose keys and values ``write`` then brings."""
-        p, n = self._list(seqs, "seqs"), seqs.shape[0]
-        c, s = self._list(counts, "counts", n), self._where(stream)
+        n = self._entries(seqs, "seqs")
+        p, c, s = self._list(seqs, "seqs", n), self._list(counts, "counts", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_extend(self._ref, n, m, p, c, s), "exl3_kv_extend")
+            st = _extend(self._ref, n, m, p, c, s)
+            if st:
+                ex._check(st, "exl3_kv_extend")
 
     def write(self, layer: int, seqs: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               counts: Optional[torch.Tensor] = None, stream=None):
         """Keys and values (n, m, n_heads, head_dim) of the last m (counts:
         counts[b]) tokens of each sequence, in one layer."""
-        p, n = self._list(seqs, "seqs"), seqs.shape[0]
-        c = self._list(counts, "counts", n)
+        n = self._entries(seqs, "seqs")
+        p, c = self._list(seqs, "seqs", n), self._list(counts, "counts", n)
         m, bs, rs = self._rows(k, "k", n, self.n_heads)
         if not self._alike(v, k):
             raise ValueError("k and v must have the same type, device, shape and strides")
         s = self._where(stream)
         if n and m:
-            ex._check(ex.lib.exl3_kv_write(self._ref, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s),
-                      "exl3_kv_write")
+            st = _write(self._ref, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s)
+            if st:
+                ex._check(st, "exl3_kv_write")
 
     def truncate(self, seqs: torch.Tensor, lens: Optional[torch.Tensor] = None, stream=None):
         """Each sequence keeps its first lens[b] tokens (None: it is freed)."""
-        p, n = self._list(seqs, "seqs"), seqs.shape[0]
-        c, s = self._list(lens, "lens", n), self._where(stream)
+        n = self._entries(seqs, "seqs")
+        p, c, s = self._list(seqs, "seqs", n), self._list(lens, "lens", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_truncate(self._ref, n, p, c, s), "exl3_kv_truncate")
+            st = _truncate(self._ref, n, p, c, s)
+            if st:
+                ex._check(st, "exl3_kv_truncate")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Each empty sequence dst[b] shares all of src[b] from now on."""
-        p, n = self._list(src, "src"), src.shape[0]
-        d, s = self._list(dst, "dst", n), self._where(stream)
+        n = self._entries(src, "src")
+        p, d, s = self._list(src, "src", n), self._list(dst, "dst", n), self._where(stream)
         if n:
-            ex._check(ex.lib.exl3_kv_fork(self._ref, n, p, d, s), "exl3_kv_fork")
+            st = _fork(self._ref, n, p, d, s)
+            if st:
+                ex._check(st, "exl3_kv_fork")
 
     def compact(self, stream=None):
         """Moves pages so that the used ones are the first of the pool."""
-        ex._check(ex.lib.exl3_kv_compact(self._ref, self._where(stream)), "exl3_kv_compact")
+        st = _compact(self._ref, self._where(stream))
+        if st:
+            ex._check(st, "exl3_kv_compact")
 
     # --------------------------------------------------------- attention ---
 
@@ -207,8 +227,8 @@ class KvCache:
         default.  lse: (n, m, n_q_heads) fp32, filled with the logarithms of
         the softmax sums.  Rows from counts[b] on are left as they were (in an
         ``out`` made here: zero)."""
-        p, n = self._list(seqs, "seqs"), seqs.shape[0]
-        c = self._list(counts, "counts", n)
+        n = self._entries(seqs, "seqs")
+        p, c = self._list(seqs, "seqs", n), self._list(counts, "counts", n)
         heads = q.shape[2] if q.dim() == 4 else 0
         m, qb, qr = self._rows(q, "q", n, heads)
         if out is None:
@@ -227,8 +247,9 @@ class KvCache:
             return out
         if workspace is None:
             workspace = self.attention_workspace(n, m, heads)
-        ex._check(ex.lib.exl3_paged_attention(
-            self._ref, layer, n, m, p, c, q.data_ptr(), qb, qr, heads, self._scale if scale is None else scale, window,
-            sinks, out.data_ptr(), ob, orow, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-            ex._room(workspace, self._index), s), "exl3_paged_attention")
+        st = _attention(self._ref, layer, n, m, p, c, q.data_ptr(), qb, qr, heads, self._scale if scale is None else scale,
+                        window, sinks, out.data_ptr(), ob, orow, None if lse is None else lse.data_ptr(),
+                        workspace.data_ptr(), ex._room(workspace, self._index), s)
+        if st:
+            ex._check(st, "exl3_paged_attention")
         return out
