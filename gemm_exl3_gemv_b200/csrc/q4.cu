@@ -442,38 +442,42 @@ __global__ void __launch_bounds__(256) q4_pack_kernel(const uint8_t* __restrict_
 // channels, so that x is read less often: a CTA then takes 8 m channels and
 // more, and x is at most half the bytes of the weights.
 struct Q4Plan {
-    int shape, ct, rows, warps_c, blocks, splits, depth;
+    int shape, ct, warps_c, blocks, splits;
 };
+
+constexpr int most_rows(int shape) { return shape == 0 ? 2 : 8 * shape; }
+constexpr int least_warps_c(int shape) { return shape == 0 ? 1 : shape == 1 ? 2 : 4; }
 
 Q4Plan q4_plan(int m, int k_in, int n_out)
 {
     Q4Plan pl;
     pl.shape = m <= 2 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : m <= 24 ? 3 : 4;
     pl.ct = pl.shape == 0 ? 1 : 2;
-    pl.rows = pl.shape <= 1 ? 8 : 8 * pl.shape;
     const int steps = (k_in / 64 + 1) / 2, tiles = (n_out / 16 + pl.ct - 1) / pl.ct;
     const int warps = 148 * 8 * 2;
     int cuts = warps / tiles;                                // of the inputs
     if (cuts > steps / 2) cuts = steps / 2;
     if (cuts < 1) cuts = 1;
-    const int least_c = pl.shape == 0 ? 1 : pl.shape == 1 ? 2 : 4;
     pl.warps_c = 8;
-    while (pl.warps_c > least_c && 16 / pl.warps_c <= cuts) pl.warps_c /= 2;
+    while (pl.warps_c > least_warps_c(pl.shape) && 16 / pl.warps_c <= cuts) pl.warps_c /= 2;
     pl.blocks = (tiles + pl.warps_c - 1) / pl.warps_c;
     pl.splits = cuts / (8 / pl.warps_c);
     if (pl.splits < 1 || pl.blocks > kMaxBlocks) pl.splits = 1;
     return pl;
 }
 
-template <int CT, int NT, int SPS, int GROUP>
+template <int SHAPE, int CT, int NT, int SPS, int GROUP>
 cudaError_t launch_q4_t(Q4Args a, const Q4Plan& pl, cudaStream_t stream)
 {
     using S = Q4Shape<CT, NT, SPS, GROUP>;
     auto kern = q4_gemm_kernel<CT, NT, SPS, GROUP>;
-    // as many stages as fit beside kMinCtas - 1 other CTAs on an SM
+    // as many stages as fit beside kMinCtas - 1 other CTAs on an SM, whose 228 KB hold 1 KB of the system's a CTA;
+    // two at least, whatever the rows and the cut
     const int stage = S::kWarps * S::kStage + S::kWarps / pl.warps_c * a.m * S::kXRow;
-    constexpr int kRoom = 227 * 1024 / S::kMinCtas - 3072;
-    a.depth = kRoom / stage;                                 // two at least: the largest stage takes half of kRoom
+    constexpr int kRoom = 227 * 1024 / S::kMinCtas - 1024;
+    static_assert(2 * (S::kWarps * S::kStage + S::kWarps / least_warps_c(SHAPE) * most_rows(SHAPE) * S::kXRow) <= kRoom,
+                  "a ring needs two stages");
+    a.depth = kRoom / stage;
     if (a.depth > kQ4MaxDepth) a.depth = kQ4MaxDepth;
     const int join = (int)sizeof(float) * S::kWarps * 16 * CT * S::kRows;
     const int smem = a.depth * stage > join ? a.depth * stage : join;
@@ -485,11 +489,11 @@ cudaError_t launch_q4_t(Q4Args a, const Q4Plan& pl, cudaStream_t stream)
     return launch_pdl(kern, dim3((unsigned)pl.blocks, (unsigned)pl.splits), dim3(S::kThreads), (size_t)smem, stream, a);
 }
 
-template <int CT, int NT, int SPS>
+template <int SHAPE, int CT, int NT, int SPS>
 cudaError_t launch_q4_g(const Q4Args& a, const Q4Plan& pl, int group, cudaStream_t stream)
 {
-    return group == 32 ? launch_q4_t<CT, NT, SPS, 32>(a, pl, stream)
-                       : group == 64 ? launch_q4_t<CT, NT, SPS, 64>(a, pl, stream) : launch_q4_t<CT, NT, SPS, 128>(a, pl, stream);
+    return group == 32 ? launch_q4_t<SHAPE, CT, NT, SPS, 32>(a, pl, stream)
+                       : group == 64 ? launch_q4_t<SHAPE, CT, NT, SPS, 64>(a, pl, stream) : launch_q4_t<SHAPE, CT, NT, SPS, 128>(a, pl, stream);
 }
 
 }  // namespace
@@ -508,11 +512,11 @@ cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, con
     const Q4Plan pl = q4_plan(m, k_in, n_out);
     const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws};
     switch (pl.shape) {
-        case 0: return launch_q4_g<1, 1, 4>(a, pl, group, stream);
-        case 1: return launch_q4_g<2, 1, 2>(a, pl, group, stream);
-        case 2: return launch_q4_g<2, 2, 2>(a, pl, group, stream);
-        case 3: return launch_q4_g<2, 3, 1>(a, pl, group, stream);
-        default: return launch_q4_g<2, 4, 1>(a, pl, group, stream);
+        case 0: return launch_q4_g<0, 1, 1, 4>(a, pl, group, stream);
+        case 1: return launch_q4_g<1, 2, 1, 2>(a, pl, group, stream);
+        case 2: return launch_q4_g<2, 2, 2, 2>(a, pl, group, stream);
+        case 3: return launch_q4_g<3, 2, 3, 1>(a, pl, group, stream);
+        default: return launch_q4_g<4, 2, 4, 1>(a, pl, group, stream);
     }
 }
 

@@ -62,6 +62,16 @@ def test_q4_large(ex, m, k, n):
     close(on_gpu(ex, c, fp32=True), *reference(c), True)
 
 
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("m", [2, 8, 16, 24, 32])
+def test_q4_narrow_and_deep(ex, m, group):
+    """Few channels and many inputs, cut as finely as it goes along the inputs: at the most rows of a kernel
+    shape the stages of the rings are at their largest."""
+    for k, n in ((8192, 64), (4160, 272)):
+        c = make(m, k, n, group, seed=m + n)
+        close(on_gpu(ex, c, fp32=True), *reference(c), True)
+
+
 def test_q4_pack_layout(ex):
     """Every word of the packed tiles, field by field from the documented layout."""
     import torch
