@@ -574,6 +574,15 @@ extern "C" int exl3_kv_compact(const exl3_kv_cache_t* cache, void* stream)
 
 namespace {
 
+// Whether the rows of an n x m array of rows of `row` elements lie apart.
+bool rows_apart(int n, int m, long long row, long long batch_stride, long long row_stride)
+{
+    if (n == 1 || m == 1) return (n == 1 || batch_stride >= row) && (m == 1 || row_stride >= row);
+    const bool batch_outer = batch_stride >= row_stride;
+    const long long inner = batch_outer ? row_stride : batch_stride, outer = batch_outer ? batch_stride : row_stride;
+    return inner >= row && (outer - row) / inner >= (batch_outer ? m : n) - 1;
+}
+
 bool attention_heads_ok(int n_q_heads, int n_heads) { return n_q_heads % n_heads == 0 && n_q_heads / n_heads <= 32; }
 
 }  // namespace
@@ -609,6 +618,7 @@ extern "C" int exl3_paged_attention(const exl3_kv_cache_t* cache, int layer, int
     if (st != EXL3_OK) return st;
     if (layer >= t.c.n_layers) return EXL3_ERR_INVALID_ARG;
     if (m > 32 || !attention_heads_ok(n_q_heads, t.c.n_heads)) return EXL3_ERR_UNSUPPORTED;
+    if (!rows_apart(n, m, (long long)n_q_heads * t.c.head_dim, out_batch_stride, out_row_stride)) return EXL3_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || q_batch_stride % 8 || q_row_stride % 8 ||
         out_batch_stride % 8 || out_row_stride % 8)
         return EXL3_ERR_MISALIGNED;

@@ -249,15 +249,26 @@ __global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n,
 // ------------------------------------------------------------------ write ---
 // A thread moves 16 bytes of a key and of a value.  Bound by memory; what the
 // places cost (sequence, length, page: three dependent loads) is shared by the
-// 16 pieces of a row through the L1.
+// 16 pieces of a row through the L1.  Every CTA checks the whole list first, as
+// a repeated sequence would be written by two entries in no order.
 
 __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int n, int m, const int* seqs, const int* counts,
                                                        const uint16_t* k_new, const uint16_t* v_new, long long bs,
                                                        long long rs)
 {
+    extern __shared__ uint32_t seen[];
+    for (int i = threadIdx.x; i < (a.n_seqs + 31) / 32; i += blockDim.x) seen[i] = 0;
     grid_dep_wait();
     grid_dep_launch();
-    const int old_fault = __ldcg(a.scratch + kKvFault);      // looked at once the places' loads are on their way
+    const int old_fault = __ldcg(a.scratch + kKvFault);
+    __syncthreads();
+    bool bad = false;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, seqs[e], a.n_seqs) || (counts && counts[e] > m);
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) fault(a, kKvIndex);
+        return;
+    }
+    if (old_fault) return;
     const int row_vec = a.n_heads * a.head_dim / 8, head_vec = a.head_dim / 8, ps = a.page_size;
     const long long all = (long long)n * m * row_vec;
     const long long page_el = (long long)a.n_heads * ps * a.head_dim;
@@ -266,9 +277,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int 
         const long long r = i / row_vec;
         const int b = (int)(r / m), row = (int)(r % m);
         const int c = counts ? counts[b] : m, s = seqs[b];
-        if (old_fault) return;
         if (row >= c) continue;
-        if (c > m || s < 0 || s >= a.n_seqs) { fault(a, kKvIndex); continue; }
         const int pos = a.lens[s] - c + row;
         if (pos < 0 || pos >= a.max_pages * ps) { fault(a, kKvIndex); continue; }
         const int page = a.table[(long long)s * a.max_pages + pos / ps];
@@ -511,8 +520,8 @@ cudaError_t launch_kv_write(const KvArgs& a, int layer, int n, int m, const int*
                             long long row_stride, cudaStream_t stream)
 {
     const long long pieces = (long long)n * m * a.n_heads * a.head_dim / 8, blocks = (pieces + 255) / 256;
-    return launch_pdl(kv_write_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)), dim3(256), 0, stream, a,
-                      layer, n, m, seqs, counts, k_new, v_new, batch_stride, row_stride);
+    return launch_pdl(kv_write_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)), dim3(256), seen_bytes(a),
+                      stream, a, layer, n, m, seqs, counts, k_new, v_new, batch_stride, row_stride);
 }
 
 cudaError_t launch_kv_truncate(const KvArgs& a, int n, const int* seqs, const int* new_lens, cudaStream_t stream)

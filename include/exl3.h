@@ -328,7 +328,10 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  *   4*c + 8*(i/2) + 16*(i%2).
  * The weights enter the tensor cores as exact integers q - zero, products are
  * summed in fp32, and each group's sum is scaled in fp32.  The order of every
- * sum is fixed: repeated calls are bitwise identical.
+ * sum is fixed: repeated calls are bitwise identical.  An infinity or NaN in a
+ * row of x makes outputs of that row infinite or NaN (which of the two depends
+ * on m: up to 8 rows the zero point is taken off the group's sum), and touches
+ * no other row.
  */
 EXL3_API size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out);
 EXL3_API int exl3_q4_gemm(int m, const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
@@ -373,6 +376,8 @@ EXL3_API int exl3_q4_pack(const uint8_t *q, int k_in, int n_out, uint32_t *packe
  * lengths need only 4-byte alignment).  They are checked on the
  * device: a number out of range or a repeated one makes the whole call do
  * nothing and is reported by exl3_kv_status as EXL3_ERR_INDEX.
+ * (exl3_paged_attention, which changes nothing, answers a repeated number twice
+ * and leaves out the rows of a bad one.)
  */
 typedef struct exl3_kv_cache {
     uint16_t *k;
@@ -462,7 +467,7 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  *   q    : row i of entry b at element b*q_batch_stride + i*q_row_stride,
  *          n_q_heads x head_dim fp16.   n_q_heads : a multiple of n_heads, at
  *          most 32 of them per head of the cache.
- *   out  : as q, with its own strides.   lse : n x m x n_q_heads fp32, the
+ *   out  : as q, with its own strides, whose rows must not overlap.   lse : n x m x n_q_heads fp32, the
  *          natural logarithm of each softmax's sum of exponentials; or NULL.
  *   scale: finite.   window, sinks : >= 0.
  *   workspace, ws_bytes : at least exl3_paged_attention_workspace_bytes(...)

@@ -78,7 +78,7 @@ def test_write(ex):
 def test_attention(ex):
     f, c = ex.lib.exl3_paged_attention, cache(ex)
     ok = dict(layer=0, n=1, m=2, seqs=16, counts=0, q=16, qb=0, qr=0, heads=8, scale=1.0, window=0, sinks=0, out=16, ob=0,
-              orow=0, lse=0, ws=256, room=1 << 30)
+              orow=1024, lse=0, ws=256, room=1 << 30)
 
     def call(**kw):
         a = {**ok, **kw}
@@ -92,10 +92,16 @@ def test_attention(ex):
         assert call(**kw) == ex.EXL3_ERR_INVALID_ARG, kw
     for kw in (dict(m=33), dict(heads=6), dict(heads=132), dict(n=1025)):
         assert call(**kw) == ex.EXL3_ERR_UNSUPPORTED, kw
-    for kw in (dict(q=24), dict(out=24), dict(lse=20), dict(qb=4), dict(qr=4), dict(ob=4), dict(orow=4), dict(ws=16), dict(counts=3)):
+    for kw in (dict(q=24), dict(out=24), dict(lse=20), dict(qb=4), dict(qr=4), dict(ob=4), dict(orow=1028), dict(ws=16), dict(counts=3)):
         assert call(**kw) == ex.EXL3_ERR_MISALIGNED, kw
     for kw in (dict(ws=0), dict(room=need - 1)):
         assert call(**kw) == ex.EXL3_ERR_WORKSPACE, kw
+    # rows of the result (1024 elements each) must lie apart
+    for kw in (dict(orow=0), dict(orow=1016), dict(n=2, ob=1024), dict(n=2, ob=2040), dict(n=2, ob=0), dict(n=2, m=1, ob=1016),
+               dict(n=3, ob=1024, orow=2048), dict(n=3, ob=1024, orow=3064)):
+        assert call(**kw) == ex.EXL3_ERR_INVALID_ARG, kw
+    for kw in (dict(m=1, orow=0), dict(n=2, ob=2048), dict(n=2, m=1, ob=1024, orow=0), dict(n=3, ob=1024, orow=3 * 1024)):
+        assert call(**kw, ws=0) == ex.EXL3_ERR_WORKSPACE, kw      # refused for the workspace alone
 
 
 def test_sizes(ex):

@@ -308,6 +308,13 @@ def test_bad_numbers_are_not_followed(ex):
     check(c.run(), [1, 2])
 
 
+def test_a_repeated_sequence_is_answered_twice(ex):
+    c = Case([700, 90], [2, 2], m=2, page=64, seed=19)
+    c.seqs, c.counts, c.lens = [0, 1, 0], [2, 2, 2], [700, 90]
+    c.q = np.concatenate([c.q, c.q[:1] * 0.5])
+    c.check(c.run())
+
+
 def test_refusals(ex):
     import torch
     c = Case([30, 77], [1, 1], dim=64, seed=17)
@@ -322,6 +329,7 @@ def test_refusals(ex):
             call()
     for call, status in ((lambda: a(1, seqs, q), ex.EXL3_ERR_INVALID_ARG), (lambda: a(0, seqs, q, window=-1), ex.EXL3_ERR_INVALID_ARG),
                          (lambda: a(0, seqs, q, sinks=-1), ex.EXL3_ERR_INVALID_ARG),
+                         (lambda: a(0, seqs, q, out=q[:1].expand(2, -1, -1, -1)), ex.EXL3_ERR_INVALID_ARG),
                          (lambda: a(0, seqs, q, scale=float("nan")), ex.EXL3_ERR_INVALID_ARG),
                          (lambda: a(0, seqs, q[:, :, :5].contiguous()), ex.EXL3_ERR_UNSUPPORTED),
                          (lambda: a(0, seqs, q.repeat(1, 33, 1, 1)), ex.EXL3_ERR_UNSUPPORTED),

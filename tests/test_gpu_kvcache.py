@@ -247,6 +247,51 @@ def test_refused_steps_change_nothing(ex):
     p.check()
 
 
+def test_refused_writes_change_nothing(ex):
+    """A write by itself, with a bad or repeated number, or more tokens than rows."""
+    import torch
+    p = Pair(pages=10, seqs=4, max_pages=6)
+    p.grow([0, 1], [20, 30])
+    kv = torch.ones(2, 9, 2, 64, dtype=torch.float16, device="cuda")
+    for seqs, counts in (([0, 4], None), ([-1, 0], None), ([1, 1], None), ([0, 0], [1, 0]), ([1, 0], [3, 10]),
+                         ([0, 2 ** 31 - 1], None)):
+        p.gpu.write(1, p.ids(seqs), kv, kv, counts=None if counts is None else p.ids(counts))
+        p.check(ex.EXL3_ERR_INDEX)
+
+
+def test_offsets_past_32_bits(ex):
+    """A pool of 2.5e9 elements (5 GB) of keys: sequences whose pages lie at its end are grown, forked, copied
+    and written, attended to, moved to its front by a compaction, and attended to again."""
+    import torch
+    import cache_model
+    from gemm_exl3_gemv_b200.kvcache import KvCache
+    heads, ps, dim, pages = 8, 64, 128, 38400
+    ids = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    c = KvCache.empty(1, pages, heads, ps, dim, 3, pages)
+    assert c.k.numel() > 2 ** 31
+    c.extend(ids(0), (pages - 8) * ps)
+    rng = np.random.default_rng(5)
+    new = lambda m: rng.standard_normal((1, m, heads, dim)).astype(np.float16)
+    dev = lambda a: torch.from_numpy(a).cuda()
+    k1, v1, k2, v2, q = new(100), new(100), new(70), new(70), rng.standard_normal((2, 3, 16, dim)).astype(np.float16)
+    c.extend(ids(1), 100)
+    c.write(0, ids(1), dev(k1), dev(v1))
+    c.fork(ids(1), ids(2))
+    c.extend(ids(2), 70)                                      # its last page is copied
+    c.write(0, ids(2), dev(k2), dev(v2))
+    assert c.table[1, :2].tolist() == [pages - 8, pages - 7] and c.table[2, :3].tolist() == [pages - 8, pages - 6, pages - 5]
+    out = c.attention(0, ids(1, 2), dev(q))
+    cat = lambda a, b: np.concatenate([a[0], b[0]]).astype(np.float64)
+    for b, (k, v) in enumerate(((k1[0].astype(np.float64), v1[0].astype(np.float64)), (cat(k1, k2), cat(v1, v2)))):
+        ref, _, tol, _ = cache_model.attention(q[b].astype(np.float64), k, v, len(k) - 3, dim ** -0.5)
+        assert np.all(np.abs(out[b].double().cpu().numpy() - ref) <= tol)
+    c.truncate(ids(0))
+    c.compact()
+    assert c.table[1, :2].tolist() == [0, 1] and c.table[2, :3].tolist() == [0, 2, 3]
+    assert torch.equal(c.attention(0, ids(1, 2), dev(q)), out)
+    c.check()
+
+
 def test_repeated_status_reads_and_exception(ex):
     p = Pair()
     p.gpu.extend(p.ids([99]), 1)
