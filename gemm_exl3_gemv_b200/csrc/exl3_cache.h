@@ -29,6 +29,10 @@ size_t q4_workspace_bytes(int m, int k_in, int n_out);
 cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,
                            const uint8_t* zero, void* y, int y_fp32, int k_in, int n_out, int group,
                            unsigned char* ws, cudaStream_t stream);
+// The same for more rows (q4_tc.cu).
+size_t q4_tc_workspace_bytes(int m, int k_in, int n_out);
+cudaError_t launch_q4_tc(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale, const uint8_t* zero,
+                         void* y, int y_fp32, int k_in, int n_out, int group, unsigned char* ws, cudaStream_t stream);
 cudaError_t launch_q4_pack(const uint8_t* q, int k_in, int n_out, uint32_t* packed, cudaStream_t stream);
 
 // Paged key-value cache (kv_cache.cu) and the attention over it

@@ -498,8 +498,12 @@ cudaError_t launch_q4_g(const Q4Args& a, const Q4Plan& pl, int group, cudaStream
 
 }  // namespace
 
+#ifndef Q4_TC_FROM
+#define Q4_TC_FROM 9
+#endif
 size_t q4_workspace_bytes(int m, int k_in, int n_out)
 {
+    if (m >= Q4_TC_FROM) return q4_tc_workspace_bytes(m, k_in, n_out);
     const Q4Plan pl = q4_plan(m, k_in, n_out);
     if (pl.splits == 1) return ws_data_off();
     return ws_data_off() + align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256);
@@ -509,6 +513,7 @@ cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, con
                            const uint8_t* zero, void* y, int y_fp32, int k_in, int n_out, int group,
                            unsigned char* ws, cudaStream_t stream)
 {
+    if (m >= Q4_TC_FROM) return launch_q4_tc(m, x, packed, scale, zero, y, y_fp32, k_in, n_out, group, ws, stream);
     const Q4Plan pl = q4_plan(m, k_in, n_out);
     const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws};
     switch (pl.shape) {

@@ -1,0 +1,545 @@
+// q4_tc.cu -- products with plain 4-bit weights in groups (exl3_q4_gemm) on the
+// fifth-generation tensor cores.
+//
+//     y[i][n] = sum_k x[i][k] (q[k][n] - z[k/g][n]) s[k/g][n]
+//
+// A CTA takes 128 output channels, the M side of tcgen05.mma, and the rows of
+// x, up to 32, as its N side; inputs come in stages of 128.
+//   * The weights are the A operand in tensor memory.  A lane's word of the
+//     packed layout (channels g and g + 8, four inputs each) becomes four
+//     registers, one AND-OR and one packed add each: (q - z) as an exact fp16
+//     integer.  That is the register layout of tcgen05.st.16x256b: a tile of 16
+//     channels x 64 inputs, a 128-bit read a lane, is one store instruction.
+//     Nothing goes back through shared memory, whose bandwidth would be the
+//     bound (32 KB written and read again a stage); the store takes 130 clocks
+//     a stage, the eight MMAs 128 (32 rows) or 73 (16), of the 350 that the
+//     memory gives.
+//   * The order of inputs in an MMA's K is the packed layout's: 16 of 32 inputs,
+//     those of the words 2 j or 2 j + 1.  x is brought into shared memory in
+//     that order, in pieces of four inputs (8 bytes).
+//   * Each group of inputs has its own sum in tensor memory, one of several in
+//     turn.  Four warps read it, a channel a thread, scale it in fp32 and add it
+//     up.  Nothing is rounded below 32 bits before the result.
+// Eight warps bring words, zero points and x by cp.async, several stages ahead,
+// and decode; one warp issues the MMAs.  CTAs that split the inputs are joined
+// in order by the last one to arrive.
+#include <cuda_fp16.h>
+
+#include "exl3_cache.h"
+#include "exl3_tc.cuh"
+
+#ifndef Q4_LEAST
+#define Q4_LEAST 3
+#endif
+namespace exl3 {
+
+namespace {
+
+struct Q4TcArgs {
+    const uint16_t* x;
+    const uint32_t* packed;
+    const uint16_t* scale;
+    const uint8_t* zero;
+    void* y;
+    int m, k_in, n_out, y_fp32;
+    int splits;
+    unsigned char* ws;
+    const unsigned char* xt;  // x as the stages want it, in the workspace
+    float* parts;             // partial sums, in the workspace
+};
+
+// Warps: two sets of eight decoders, of four scalers and of one that issues MMAs
+// take stages in turn; one brings x.
+constexpr int kSets = 2, kDecoders = 8, kScalers = 4;        // of a set
+constexpr int kFirstScaler = kSets * kDecoders, kBringer = kFirstScaler + kSets * kScalers, kFirstIssuer = kBringer + 1;
+constexpr int kTcThreads = 32 * (kFirstIssuer + kSets);
+constexpr int kScaleRing = 16;                               // groups
+
+template <int N>
+constexpr int kXStage = 2 * N * 128;                         // bytes of x of a stage: two halves of 64 inputs, 128-byte swizzle
+
+template <int N, int GROUP>
+struct Q4Tc {
+    static constexpr int kParts = 128 / GROUP;               // groups of a stage
+    static constexpr int kRing = 8;                          // stages of x in shared memory
+    static constexpr int kA = 4;                             // stages of weights in tensor memory
+    static constexpr int kD = 8;                             // sums of groups in turn
+    static constexpr int kCols = 512;
+    static constexpr int kSums = 64 * kA;                    // first column of the sums
+    static_assert(kSums + kD * N <= kCols);
+    static_assert(kRing % kA == 0 && kA % kSets == 0 && kRing * kParts % kD == 0 && kD % (kSets * kParts) == 0);
+    static constexpr int kWords = 1024, kOwn = kWords + 16 * kParts;             // of a decoder's stage
+    static constexpr int kOwnRing = 8;                       // stages of a decoder in shared memory
+    static constexpr int kXAll = kRing * kXStage<N>, kOwnAll = kOwnRing * kSets * kDecoders * kOwn;
+    static constexpr int kOther = N * 128 * 4;               // the second set's sums
+    static constexpr int kScales = kSets * kScalers * kScaleRing * 64;
+    static constexpr int kSmem = kXAll + kOwnAll + kOther + kScales + 512;
+    static_assert(kSmem <= 227 * 1024);
+};
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// The pair's fields in the mantissa of 1024, in one instruction.
+__device__ __forceinline__ __half2 masked_1024(uint32_t w, uint32_t mask)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return bits_h2(r);
+}
+
+// A word as the fp16 pairs q - z of channel g (inputs 0 1, 2 3) and g + 8, from
+// 1024 + q and 1024 + 16 q: zlo = -(1024 + z), zhi = -(64 + z).
+__device__ __forceinline__ void decode_word(uint32_t w, __half2 zlo, __half2 zhi, uint32_t* a)
+{
+    const uint32_t v = w >> 8;
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    a[0] = h2_bits(__hadd2(masked_1024(w, 0x000F000Fu), zlo));
+    a[1] = h2_bits(__hadd2(masked_1024(v, 0x000F000Fu), zlo));
+    a[2] = h2_bits(__hfma2(masked_1024(w, 0x00F000F0u), sixteenth, zhi));
+    a[3] = h2_bits(__hfma2(masked_1024(v, 0x00F000F0u), sixteenth, zhi));
+}
+
+// 16 lanes x 32 columns of tensor memory: lane (g, t) of the warp holds columns
+// 2 t and 2 t + 1 of each eight, of lane g (registers 0 1 of four) and g + 8.
+__device__ __forceinline__ void tmem_st_tile(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (+)= A B over 32 inputs, two MMAs with A in tensor memory, issued by one
+// elected lane.
+__device__ __forceinline__ void mma_f16_ts_pair_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %3, %5, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %4, %5, 1;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(a_tmem + 8), "l"(bdesc), "l"(bdesc + 2), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last GROUPS groups of this thread's copies have landed.
+template <int GROUPS>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_byte(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+// Waits that give up after 2 s: after the first that runs out the others return
+// at once.  The warp tries once; if that fails, its first lane waits, asleep:
+// twenty warps that poll would take the issue slots of the others.
+struct Patience {
+    uint32_t* status;
+    bool alive;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity)
+    {
+        if (!alive || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+        int there = 1;
+        if ((threadIdx.x & 31) == 0) {
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait_sleep(bar, parity, 1000))
+                if (global_ns() - t0 > 2000000000ull) {
+                    there = 0;
+                    atomicOr(status, kStatusTimeout);
+                    break;
+                }
+        }
+        alive = __shfl_sync(0xffffffffu, there, 0) != 0;
+    }
+};
+
+// Place and phase in a ring.
+template <int SIZE>
+struct Turn {
+    int at = 0;
+    uint32_t phase = 0;
+    template <int BY = 1>                                    // a divisor of SIZE
+    __device__ __forceinline__ void next()
+    {
+        at += BY;
+        if (at >= SIZE) {
+            at -= SIZE;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int N, int GROUP>
+__global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_constant__ Q4TcArgs p)
+{
+    using S = Q4Tc<N, GROUP>;
+    constexpr int kParts = S::kParts;
+    extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle counts rows from 1024-byte borders
+    unsigned char* own_all = smem + S::kXAll;
+    float* other = reinterpret_cast<float*>(own_all + S::kOwnAll);
+    unsigned char* scales = own_all + S::kOwnAll + S::kOther;
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + S::kScales);
+    uint64_t* done = full + S::kRing;                        // a stage's weights and x are there; its MMAs are done
+    uint64_t* d_full = done + S::kRing;                      // a group's sum is there (a stage's last: done); is read
+    uint64_t* d_empty = d_full + S::kD;
+    uint64_t* all_done = d_empty + S::kD;
+    uint32_t* tmem_base = reinterpret_cast<uint32_t*>(all_done + 1);
+    int* last_flag = reinterpret_cast<int*>(tmem_base + 1);
+    static_assert((2 * S::kRing + 2 * S::kD + 1) * 8 + 8 <= 512);
+
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+    const int kt_all = p.k_in / 64, stages = (kt_all + 1) / 2;
+    const int s0 = (int)((long long)stages * blockIdx.y / p.splits), s1 = (int)((long long)stages * (blockIdx.y + 1) / p.splits);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kRing; ++i) {
+            mbar_init(full + i, kDecoders + 1);
+            mbar_init(done + i, 1);
+        }
+        for (int i = 0; i < S::kD; ++i) {
+            mbar_init(d_full + i, 1);
+            mbar_init(d_empty + i, kScalers);
+        }
+        mbar_init(all_done, kSets);
+        fence_mbar_init();
+    }
+    // Only the warp that brings x waits for the kernel before: that one started its
+    // own dependents behind its wait, so all that came before it is done (weights
+    // may be read, and nothing that is still to run asks for tensor memory).
+    grid_dep_launch();
+    if (warp == kFirstIssuer) {
+        tmem_alloc(tmem_base, S::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_base;
+    Patience wait = {reinterpret_cast<uint32_t*>(p.ws), true};
+
+    if (warp < kFirstScaler) {
+        // ------------------------------------------------------ decoders ---
+        const int set = warp / kDecoders, quarter = warp & 3, half = (warp >> 2) & 1;   // of the 128 lanes; of a quarter's 32
+        const int tn_all = p.n_out / 16, tn = min((int)blockIdx.x * 8 + 2 * quarter + half, tn_all - 1);
+        const int first = s0 + set;
+        const uint4* words = reinterpret_cast<const uint4*>(p.packed) + ((long long)tn * kt_all + 2 * first) * 32 + lane;
+        const uint8_t* zeros = p.zero ? p.zero + (long long)(first * kParts + lane) * p.n_out + 16 * tn : nullptr;
+        const bool brings = p.zero && lane < kParts;
+        const int groups = p.k_in / GROUP;
+        const uint32_t own = smem_u32(own_all) + warp * (S::kOwnRing * S::kOwn);
+        if (!p.zero)
+            for (int i = 0; i < S::kOwnRing; ++i)
+                if (lane < 4 * kParts) asm volatile("st.shared.u32 [%0], %1;" ::"r"(own + i * S::kOwn + S::kWords + 4 * lane), "r"(0x08080808u) : "memory");
+        int fetched = first;
+        uint32_t slot = own, use = own;
+        auto fetch = [&] {                                   // this set's next stage; k_in may end on half a one
+            if (fetched < s1) {
+                copy16(slot + lane * 16, words);
+                if (2 * fetched + 1 < kt_all) copy16(slot + 512 + lane * 16, words + 32);
+                if (brings && fetched * kParts + lane < groups) copy16(slot + S::kWords + 16 * lane, zeros);
+                words += 64 * kSets;
+                if (p.zero) zeros += (long long)(kSets * kParts) * p.n_out;
+                fetched += kSets;
+            }
+            copies_commit();
+            slot = slot == own + (S::kOwnRing - 1) * S::kOwn ? own : slot + S::kOwn;
+        };
+        for (int i = 0; i < S::kOwnRing - 1; ++i) fetch();
+        // the stage's place in the ring, and that of the one whose weights lay where this one's will
+        Turn<S::kRing> here, old;
+        here.at = set;
+        old.at = (S::kRing + set - S::kA) % S::kRing;
+        old.phase = 1;
+        const uint32_t z_at = S::kWords + (lane >> 2);
+        for (int s = first; s < s1; s += kSets) {
+            copies_wait<S::kOwnRing - 2>();
+            __syncwarp();
+            fetch();                                         // to the place of this set's last stage, which every lane has read
+            wait.wait(done + old.at, old.phase);
+            tc_fence_after();
+            const uint32_t to = tmem + ((uint32_t)(32 * quarter + 16 * half) << 16) + 64 * (here.at % S::kA);
+            __half2 zlo, zhi;
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                if (tile == 1 && 2 * s + 1 >= kt_all) break;
+                const uint4 w4 = lds16(use + 512 * tile + 16 * lane);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                uint32_t r[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = 64 * tile + 32 * (j >> 1);
+                    if (j % 2 == 0 && k % GROUP == 0) {
+                        // -(1024 + z) is the bits of -1024 with z in the last places; -(64 + z) is 960 more
+                        const uint32_t z = use + z_at + 16 * (k / GROUP);
+                        zlo = bits_h2(0xE400E400u | lds_byte(z) * 0x10001u);
+                        zhi = __hadd2(bits_h2(0xE400E400u | lds_byte(z + 8) * 0x10001u), __float2half2_rn(960.f));
+                    }
+                    decode_word(w[j], zlo, zhi, r + 4 * j);
+                }
+                tmem_st_tile(to + 32 * tile, r);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + here.at);
+            here.template next<kSets>();
+            old.template next<kSets>();
+            use = use == own + (S::kOwnRing - 1) * S::kOwn ? own : use + S::kOwn;
+        }
+        copies_wait<0>();
+    } else if (warp == kBringer) {
+        // ------------------------------------------------------------- x ---
+        grid_dep_wait();                                     // the kernel before lays x out
+        // a nonzero injection word (tests of the timeout path) withholds every copy
+        const bool withhold = *reinterpret_cast<const volatile uint32_t*>(p.ws + kWsInjectOff) != 0u;
+        Turn<S::kRing> slot;
+        for (int s = s0; s < s1 && !withhold; ++s) {
+            wait.wait(done + slot.at, slot.phase ^ 1);
+            if (!wait.alive) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full + slot.at, kXStage<N>);
+                bulk_g2s(smem + slot.at * kXStage<N>, p.xt + (size_t)s * kXStage<N>, kXStage<N>, full + slot.at);
+            }
+            __syncwarp();
+            slot.next();
+        }
+    } else if (warp < kBringer) {
+        // ------------------------------------------------------- scalers ---
+        const int set = (warp - kFirstScaler) / kScalers, quarter = warp & 3, ch0 = blockIdx.x * 128 + 32 * quarter, ch = ch0 + lane;
+        const int first = s0 + set, groups = p.k_in / GROUP;
+        const uint32_t ring = smem_u32(scales) + (warp - kFirstScaler) * (kScaleRing * 64);
+        const uint16_t* from = p.scale + (long long)first * kParts * p.n_out + ch0 + 8 * lane;
+        const bool brings = lane < 4 && ch0 + 8 * lane < p.n_out;
+        int f_group = first * kParts, f_slot = 0, slot = 0;
+        auto fetch = [&] {
+            if (f_group < min(s1 * kParts, groups) && brings) copy16(ring + f_slot * 64 + 16 * lane, from);
+            copies_commit();
+            const int by = f_group % kParts == kParts - 1 ? (kSets - 1) * kParts + 1 : 1;    // from a stage's last to the set's next stage
+            from += (long long)by * p.n_out;
+            f_group += by;
+            f_slot = (f_slot + 1) & (kScaleRing - 1);
+        };
+        for (int i = 0; i < kScaleRing - 1; ++i) fetch();
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        Turn<S::kRing> here;
+        Turn<S::kD / kParts> d;                              // a stage's sums
+        here.at = d.at = set;
+        for (int s = first; s < s1; s += kSets) {
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                const int gr = s * kParts + part;
+                if (gr >= groups) break;
+                copies_wait<kScaleRing - 2>();
+                __syncwarp();
+                fetch();                                     // to the place of the group before, which every lane has read
+                uint16_t sh;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sh) : "r"(ring + slot * 64 + 2 * lane));
+                slot = (slot + 1) & (kScaleRing - 1);
+                const float sc = __half2float(__ushort_as_half(sh));
+                const int sum = d.at * kParts + part;
+                if (part == kParts - 1 || gr == groups - 1) wait.wait(done + here.at, here.phase);
+                else wait.wait(d_full + sum, d.phase);
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < N; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + S::kSums + sum * N + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c + i] += sc * __uint_as_float(r[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(d_empty + sum);
+            }
+            here.template next<kSets>();
+            d.template next<kSets>();
+        }
+        copies_wait<0>();
+        // the sets' sums
+        float* mine = other + 32 * quarter + lane;
+        if (set == 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) mine[i * 128] = acc[i];
+        }
+        named_bar(2, 32 * kSets * kScalers);
+        if (set == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] += mine[i * 128];
+        // ---- the result, or a part of it ----
+        bool write = true;
+        float* parts = p.parts + (size_t)blockIdx.x * p.splits * p.m * 128 + 32 * quarter + lane;
+        if (p.splits > 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < p.m) __stcg(parts + ((size_t)blockIdx.y * p.m + i) * 128, acc[i]);
+            named_bar(1, 32 * kScalers);
+            if (threadIdx.x == 32 * kFirstScaler) {
+                uint32_t* counter = reinterpret_cast<uint32_t*>(p.ws + ws_counter_off()) + blockIdx.x;
+                __threadfence();
+                *last_flag = atomicAdd(counter, 1u) == (uint32_t)p.splits - 1;
+                if (*last_flag) *counter = 0;
+                __threadfence();
+            }
+            named_bar(1, 32 * kScalers);
+            write = *last_flag != 0;
+            if (write) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = i < p.m ? __ldcg(parts + (size_t)i * 128) : 0.f;
+                for (int v = 1; v < p.splits; ++v)
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (i < p.m) acc[i] += __ldcg(parts + ((size_t)v * p.m + i) * 128);
+            }
+        }
+        if (write && ch < p.n_out) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < p.m) {
+                    if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = acc[i];
+                    else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(acc[i]);
+                }
+        }
+        }
+    } else {
+        // ----------------------------------------------------- MMA warps ---
+        // Unrolled over the ring, so that addresses are a base and constants: what
+        // these warps execute is the longest chain of a stage (two of them took the
+        // 32-row case from @ to @ us).
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);     // f32 += f16 x f16, both K-major
+        const int set = warp - kFirstIssuer;
+        const uint64_t x0 = sdesc_sw128(smem_u32(smem) + set * kXStage<N>, 16, 1024);
+        const uint32_t a0 = tmem + 64 * set, sum0 = set * kParts, d0 = tmem + S::kSums + sum0 * N;
+        uint32_t round = 0;                                  // of the ring: its parity is the barriers' phase
+        for (int base = s0 + set; base < s1 && wait.alive; base += S::kRing, ++round) {
+#pragma unroll
+            for (int i = 0; i < S::kRing; i += kSets) {
+                if (base + i >= s1) break;
+                const bool whole = 2 * (base + i) + 1 < kt_all;
+                wait.wait(full + set + i, round & 1);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    if (part * GROUP >= 64 && !whole) break;
+                    const int sum = (i * kParts + part) % S::kD;
+                    wait.wait(d_empty + sum0 + sum, (round * (S::kRing * kParts / S::kD) + i * kParts / S::kD + 1) & 1);
+                    tc_fence_after();
+                    if (!wait.alive) break;
+#pragma unroll
+                    for (int k = part * GROUP; k < (part + 1) * GROUP; k += 32)
+                        if (k < 64 || whole)
+                            mma_f16_ts_pair_elect(d0 + sum * N, a0 + 64 * (i % S::kA) + k / 2,
+                                                  x0 + (i * kXStage<N> + (k >> 6) * (N * 128) + 2 * (k & 63)) / 16, idesc, k > part * GROUP);
+                    if (part < kParts - 1) mma_commit_elect(d_full + sum0 + sum);
+                }
+                if (wait.alive) mma_commit_elect(done + set + i);
+            }
+        }
+        mma_commit_elect(all_done);                          // before tensor memory is given back
+        (void)mbar_wait_bounded(all_done, 0, 100000000ull);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kFirstIssuer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kCols);
+    }
+}
+
+// x in the order of the stages' shared memory: per stage and half (64 inputs) N
+// rows of 128 bytes, swizzled, K-step by K-step, each of the inputs that a word of
+// the packed layout holds.  A thread writes 16 bytes, two pieces of four inputs;
+// rows past the last one are zero.
+template <int N>
+__global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* x, int m, int k_in, unsigned char* xt)
+{
+    grid_dep_wait();
+    grid_dep_launch();                                       // behind the wait: the product may then read its weights at once
+    const int i = blockIdx.x * 256 + threadIdx.x, chunk = i & 7, row = (i >> 3) % N, half = i / (8 * N);
+    if (half >= k_in / 64) return;
+    const int k = 64 * half + 32 * (chunk >> 2) + 4 * ((chunk >> 1) & 1) + 16 * (chunk & 1);
+    uint2 lo = make_uint2(0, 0), hi = lo;
+    if (row < m) {
+        const uint2* from = reinterpret_cast<const uint2*>(x + (long long)row * k_in + k);
+        lo = from[0];
+        hi = from[2];
+    }
+    *reinterpret_cast<uint4*>(xt + (size_t)half * (N * 128) + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+template <int N, int GROUP>
+cudaError_t launch_t(const Q4TcArgs& a, int blocks, cudaStream_t stream)
+{
+    using S = Q4Tc<N, GROUP>;
+    auto kern = q4_tc_kernel<N, GROUP>;
+    static std::atomic<int> done[kMaxDevices];
+    const cudaError_t e = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const cudaError_t ex = launch_pdl(q4_x_kernel<N>, dim3((unsigned)((a.k_in / 64 * 8 * N + 255) / 256)), dim3(256), 0, stream, a.x,
+                                      a.m, a.k_in, const_cast<unsigned char*>(a.xt));
+    if (ex != cudaSuccess) return ex;
+    return launch_pdl(kern, dim3((unsigned)blocks, (unsigned)a.splits), dim3(kTcThreads), S::kSmem, stream, a);
+}
+
+template <int N>
+cudaError_t launch_n(const Q4TcArgs& a, int group, int blocks, cudaStream_t stream)
+{
+    return group == 32 ? launch_t<N, 32>(a, blocks, stream) : group == 64 ? launch_t<N, 64>(a, blocks, stream) : launch_t<N, 128>(a, blocks, stream);
+}
+
+struct Q4TcPlan {
+    int blocks, splits;
+    size_t x_bytes(int m, int k_in) const { return (size_t)(k_in / 64 + 1) / 2 * (m > 16 ? kXStage<32> : kXStage<16>); }
+};
+
+Q4TcPlan q4_tc_plan(int k_in, int n_out)
+{
+    const int blocks = (n_out + 127) / 128, stages = (k_in / 64 + 1) / 2;
+    int splits = 148 / blocks;
+    if (splits > (stages + Q4_LEAST - 1) / Q4_LEAST) splits = (stages + Q4_LEAST - 1) / Q4_LEAST;
+    return Q4TcPlan{blocks, splits < 1 ? 1 : splits};
+}
+
+}  // namespace
+
+size_t q4_tc_workspace_bytes(int m, int k_in, int n_out)
+{
+    const Q4TcPlan pl = q4_tc_plan(k_in, n_out);
+    return ws_data_off() + pl.x_bytes(m, k_in) + (pl.splits == 1 ? 0 : align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * m * 128, 256));
+}
+
+cudaError_t launch_q4_tc(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale, const uint8_t* zero,
+                         void* y, int y_fp32, int k_in, int n_out, int group, unsigned char* ws, cudaStream_t stream)
+{
+    const Q4TcPlan pl = q4_tc_plan(k_in, n_out);
+    unsigned char* xt = ws + ws_data_off();
+    const Q4TcArgs a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws, xt,
+                        reinterpret_cast<float*>(xt + pl.x_bytes(m, k_in))};
+    return m > 16 ? launch_n<32>(a, group, pl.blocks, stream) : launch_n<16>(a, group, pl.blocks, stream);
+}
+
+}  // namespace exl3
