@@ -68,12 +68,13 @@ struct Q4Tc {
     static constexpr int kSums = 64 * kA;                    // first column of the sums
     static_assert(kSums + kD * N <= kCols);
     static_assert(kRing % kA == 0 && kA % kSets == 0 && kRing * kParts % kD == 0 && kD % (kSets * kParts) == 0);
-    static constexpr int kWords = 1024, kOwn = kWords + 16 * kParts;             // of a decoder's stage
+    static constexpr int kWords = 1024;                      // of a decoder's stage
     static constexpr int kOwnRing = 8;                       // stages of a decoder in shared memory
-    static constexpr int kXAll = kRing * kXStage<N>, kOwnAll = kOwnRing * kSets * kDecoders * kOwn;
-    static constexpr int kOther = N * 128 * 4;               // the second set's sums
+    static_assert(kSets == 2 && kRing == 8 && kA == 4 && kOwnRing == 8);         // the decoders' loop is written for it
+    static constexpr int kXAll = kRing * kXStage<N>, kOwnAll = kOwnRing * kSets * kDecoders * kWords;
+    static constexpr int kZeros = kSets * kDecoders * 1024;
     static constexpr int kScales = kSets * kScalers * kScaleRing * 64;
-    static constexpr int kSmem = kXAll + kOwnAll + kOther + kScales + 512;
+    static constexpr int kSmem = kXAll + kOwnAll + kZeros + kScales + 512;
     static_assert(kSmem <= 227 * 1024);
 };
 
@@ -143,6 +144,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t at)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
     return v;
 }
+// d += a b for two floats at once.
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b)
+{
+    uint64_t& dd = reinterpret_cast<uint64_t&>(d);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(dd) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+}
 __device__ __forceinline__ uint32_t lds_byte(uint32_t at)
 {
     uint32_t v;
@@ -196,8 +203,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     constexpr int kParts = S::kParts;
     extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle counts rows from 1024-byte borders
     unsigned char* own_all = smem + S::kXAll;
-    float* other = reinterpret_cast<float*>(own_all + S::kOwnAll);
-    unsigned char* scales = own_all + S::kOwnAll + S::kOther;
+    unsigned char* zero_all = own_all + S::kOwnAll;
+    unsigned char* scales = zero_all + S::kZeros;
     uint64_t* full = reinterpret_cast<uint64_t*>(scales + S::kScales);
     uint64_t* done = full + S::kRing;                        // a stage's weights and x are there; its MMAs are done
     uint64_t* d_full = done + S::kRing;                      // a group's sum is there (a stage's last: done); is read
@@ -239,72 +246,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
 
     if (warp < kFirstScaler) {
         // ------------------------------------------------------ decoders ---
+        // Unrolled over four stages of the set, one round of the ring of stages: what
+        // a stage costs beside its arithmetic is most of these warps' instructions.
         const int set = warp / kDecoders, quarter = warp & 3, half = (warp >> 2) & 1;   // of the 128 lanes; of a quarter's 32
         const int tn_all = p.n_out / 16, tn = min((int)blockIdx.x * 8 + 2 * quarter + half, tn_all - 1);
-        const int first = s0 + set;
+        const int first = s0 + set, s_whole = kt_all / 2;    // k_in may end on half a stage
+        const uint32_t own = smem_u32(own_all) + warp * (S::kOwnRing * S::kWords) + lane * 16;
         const uint4* words = reinterpret_cast<const uint4*>(p.packed) + ((long long)tn * kt_all + 2 * first) * 32 + lane;
-        const uint8_t* zeros = p.zero ? p.zero + (long long)(first * kParts + lane) * p.n_out + 16 * tn : nullptr;
-        const bool brings = p.zero && lane < kParts;
-        const int groups = p.k_in / GROUP;
-        const uint32_t own = smem_u32(own_all) + warp * (S::kOwnRing * S::kOwn);
-        if (!p.zero)
-            for (int i = 0; i < S::kOwnRing; ++i)
-                if (lane < 4 * kParts) asm volatile("st.shared.u32 [%0], %1;" ::"r"(own + i * S::kOwn + S::kWords + 4 * lane), "r"(0x08080808u) : "memory");
-        int fetched = first;
-        uint32_t slot = own, use = own;
-        auto fetch = [&] {                                   // this set's next stage; k_in may end on half a one
-            if (fetched < s1) {
-                copy16(slot + lane * 16, words);
-                if (2 * fetched + 1 < kt_all) copy16(slot + 512 + lane * 16, words + 32);
-                if (brings && fetched * kParts + lane < groups) copy16(slot + S::kWords + 16 * lane, zeros);
-                words += 64 * kSets;
-                if (p.zero) zeros += (long long)(kSets * kParts) * p.n_out;
-                fetched += kSets;
-            }
+        auto fetch = [&](int stage, int ahead, uint32_t to) {      // `ahead`: of the set's stages, from words on
+            if (stage < s1) copy16(to, words + ahead * (64 * kSets));
+            if (stage < s1 && stage < s_whole) copy16(to + 512, words + ahead * (64 * kSets) + 32);
             copies_commit();
-            slot = slot == own + (S::kOwnRing - 1) * S::kOwn ? own : slot + S::kOwn;
         };
-        for (int i = 0; i < S::kOwnRing - 1; ++i) fetch();
-        // the stage's place in the ring, and that of the one whose weights lay where this one's will
-        Turn<S::kRing> here, old;
-        here.at = set;
-        old.at = (S::kRing + set - S::kA) % S::kRing;
-        old.phase = 1;
-        const uint32_t z_at = S::kWords + (lane >> 2);
-        for (int s = first; s < s1; s += kSets) {
-            copies_wait<S::kOwnRing - 2>();
-            __syncwarp();
-            fetch();                                         // to the place of this set's last stage, which every lane has read
-            wait.wait(done + old.at, old.phase);
-            tc_fence_after();
-            const uint32_t to = tmem + ((uint32_t)(32 * quarter + 16 * half) << 16) + 64 * (here.at % S::kA);
-            __half2 zlo, zhi;
-#pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                if (tile == 1 && 2 * s + 1 >= kt_all) break;
-                const uint4 w4 = lds16(use + 512 * tile + 16 * lane);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                uint32_t r[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 64 * tile + 32 * (j >> 1);
-                    if (j % 2 == 0 && k % GROUP == 0) {
-                        // -(1024 + z) is the bits of -1024 with z in the last places; -(64 + z) is 960 more
-                        const uint32_t z = use + z_at + 16 * (k / GROUP);
-                        zlo = bits_h2(0xE400E400u | lds_byte(z) * 0x10001u);
-                        zhi = __hadd2(bits_h2(0xE400E400u | lds_byte(z + 8) * 0x10001u), __float2half2_rn(960.f));
-                    }
-                    decode_word(w[j], zlo, zhi, r + 4 * j);
-                }
-                tmem_st_tile(to + 32 * tile, r);
+        // Zero points: a copy of the warp brings 16 bytes of 32 groups, one such chunk ahead.
+        const uint32_t zero_ring = smem_u32(zero_all) + warp * 1024;
+        constexpr int kStagesOf32 = 32 / kParts;             // of the set, that have 32 groups
+        int z_group = (first + kSets * (lane / kParts)) * kParts + lane % kParts;
+        const int z_end = min(s1 * kParts, p.k_in / GROUP);
+        const uint8_t* zeros = p.zero ? p.zero + (long long)z_group * p.n_out + 16 * tn : nullptr;
+        auto fetch_zeros = [&](int chunk) {
+            if (p.zero) {
+                if (z_group < z_end) copy16(zero_ring + (chunk & 1) * 512 + 16 * lane, zeros);
+                z_group += 32 * kSets;
+                zeros += (long long)(32 * kSets) * p.n_out;
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + here.at);
-            here.template next<kSets>();
-            old.template next<kSets>();
-            use = use == own + (S::kOwnRing - 1) * S::kOwn ? own : use + S::kOwn;
+        };
+        if (!p.zero)
+            for (int i = 0; i < 8; ++i) asm volatile("st.shared.u32 [%0], %1;" ::"r"(zero_ring + 128 * i + 4 * lane), "r"(0x08080808u) : "memory");
+        fetch_zeros(0);
+        fetch_zeros(1);
+        for (int i = 0; i < S::kOwnRing - 1; ++i) fetch(first + kSets * i, i, own + i * S::kWords);
+        words += (S::kOwnRing - 1) * 64 * kSets;
+        const uint32_t to0 = tmem + ((uint32_t)(32 * quarter + 16 * half) << 16) + 64 * set;
+        uint32_t z_at = lane >> 2;
+        int n = 0;                                           // of the set's stages
+        for (int s = first; s < s1; n += 4, words += 4 * 64 * kSets) {
+            const uint32_t now = own + (n & 4) * S::kWords, then = own + (~n & 4) * S::kWords;
+#pragma unroll
+            for (int j = 0; j < 4; ++j, s += kSets) {
+                if (s >= s1) break;
+                copies_wait<S::kOwnRing - 2>();
+                __syncwarp();
+                // to the places of the stage, and of the zero points, before
+                if (j == 0 && n > 0 && n % kStagesOf32 == 0) fetch_zeros(n / kStagesOf32 + 1);
+                fetch(s + kSets * (S::kOwnRing - 1), j, (j ? now : then) + (j + 3) % 4 * S::kWords);
+                // the MMAs of the stage whose weights lay where this one's will: four stages ago
+                wait.wait(done + set + (2 * j + S::kRing - S::kA) % S::kRing, (n / 4 + (j < 2)) & 1);
+                tc_fence_after();
+                __half2 zlo, zhi;
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
+                    if (tile == 1 && s >= s_whole) break;
+                    const uint4 w4 = lds16(now + j * S::kWords + 512 * tile);
+                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 64 * tile + 32 * (i >> 1);
+                        if (i % 2 == 0 && k % GROUP == 0) {
+                            // -(1024 + z) is the bits of -1024 with z in the last places; -(64 + z) is 960 more
+                            const uint32_t z = zero_ring + z_at + 16 * (kParts * j + k / GROUP);
+                            zlo = bits_h2(0xE400E400u | lds_byte(z) * 0x10001u);
+                            zhi = __hadd2(bits_h2(0xE400E400u | lds_byte(z + 8) * 0x10001u), __float2half2_rn(960.f));
+                        }
+                        decode_word(w[i], zlo, zhi, r + 4 * i);
+                    }
+                    tmem_st_tile(to0 + 128 * (j & 1) + 32 * tile, r);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + set + 2 * j);
+            }
+            z_at = (z_at + 64 * kParts) % 1024;
         }
         copies_wait<0>();
     } else if (warp == kBringer) {
@@ -327,74 +341,82 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         // ------------------------------------------------------- scalers ---
         const int set = (warp - kFirstScaler) / kScalers, quarter = warp & 3, ch0 = blockIdx.x * 128 + 32 * quarter, ch = ch0 + lane;
         const int first = s0 + set, groups = p.k_in / GROUP;
+        // Scales: a copy of the warp brings the 64 bytes of eight groups, eight groups ahead.
         const uint32_t ring = smem_u32(scales) + (warp - kFirstScaler) * (kScaleRing * 64);
-        const uint16_t* from = p.scale + (long long)first * kParts * p.n_out + ch0 + 8 * lane;
-        const bool brings = lane < 4 && ch0 + 8 * lane < p.n_out;
-        int f_group = first * kParts, f_slot = 0, slot = 0;
+        constexpr int kStagesOf8 = 8 / kParts;               // that have eight groups
+        const int f_part = (lane >> 2) % kParts;
+        int f_stage = first + kSets * ((lane >> 2) / kParts);
+        const uint16_t* from = p.scale + ((long long)f_stage * kParts + f_part) * p.n_out + ch0 + 8 * (lane & 3);
+        const bool brings = ch0 + 8 * (lane & 3) < p.n_out;
+        uint32_t f_at = 0;
         auto fetch = [&] {
-            if (f_group < min(s1 * kParts, groups) && brings) copy16(ring + f_slot * 64 + 16 * lane, from);
+            if (brings && f_stage < s1 && f_stage * kParts + f_part < groups) copy16(ring + f_at + 16 * lane, from);
             copies_commit();
-            const int by = f_group % kParts == kParts - 1 ? (kSets - 1) * kParts + 1 : 1;    // from a stage's last to the set's next stage
-            from += (long long)by * p.n_out;
-            f_group += by;
-            f_slot = (f_slot + 1) & (kScaleRing - 1);
+            from += (long long)(kSets * 8) * p.n_out;
+            f_stage += kSets * kStagesOf8;
+            f_at = (f_at + 512) % (kScaleRing * 64);
         };
-        for (int i = 0; i < kScaleRing - 1; ++i) fetch();
-        float acc[N];
+        for (int i = 0; i < kScaleRing / 8 - 1; ++i) fetch();
+        float2 acc[N / 2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        for (int i = 0; i < N / 2; ++i) acc[i] = make_float2(0.f, 0.f);
         Turn<S::kRing> here;
         Turn<S::kD / kParts> d;                              // a stage's sums
         here.at = d.at = set;
+        uint32_t at = 2 * lane;
         for (int s = first; s < s1; s += kSets) {
+            if (at % 512 < 64) {
+                copies_wait<kScaleRing / 8 - 2>();
+                __syncwarp();                                // every lane has read the eight before, whose place is the next copy's
+                fetch();
+            }
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
                 const int gr = s * kParts + part;
                 if (gr >= groups) break;
-                copies_wait<kScaleRing - 2>();
-                __syncwarp();
-                fetch();                                     // to the place of the group before, which every lane has read
                 uint16_t sh;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sh) : "r"(ring + slot * 64 + 2 * lane));
-                slot = (slot + 1) & (kScaleRing - 1);
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sh) : "r"(ring + at + 64 * part));
                 const float sc = __half2float(__ushort_as_half(sh));
                 const int sum = d.at * kParts + part;
                 if (part == kParts - 1 || gr == groups - 1) wait.wait(done + here.at, here.phase);
                 else wait.wait(d_full + sum, d.phase);
                 tc_fence_after();
+                uint32_t r[N / 16][16];
 #pragma unroll
-                for (int c = 0; c < N; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + S::kSums + sum * N + c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[c + i] += sc * __uint_as_float(r[i]);
-                }
+                for (int c = 0; c < N / 16; ++c) tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + S::kSums + sum * N + 16 * c, r[c]);
+                tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(d_empty + sum);
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i)
+                    fma2(acc[i], make_float2(__uint_as_float(r[i / 8][2 * i % 16]), __uint_as_float(r[i / 8][2 * i % 16 + 1])), make_float2(sc, sc));
             }
+            at = (at + 64 * kParts) % (kScaleRing * 64);
             here.template next<kSets>();
             d.template next<kSets>();
         }
         copies_wait<0>();
         // the sets' sums
-        float* mine = other + 32 * quarter + lane;
+        // (through the ring of the second set's decoders, whose last stage is done)
+        float* mine = reinterpret_cast<float*>(own_all + S::kOwnAll / 2) + 32 * quarter + lane;
+        static_assert(N * 128 * 4 <= S::kOwnAll / 2);
         if (set == 1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) mine[i * 128] = acc[i];
+            for (int i = 0; i < N; ++i) mine[i * 128] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
         }
         named_bar(2, 32 * kSets * kScalers);
         if (set == 0) {
+        float y[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] += mine[i * 128];
+        for (int i = 0; i < N; ++i) y[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) + mine[i * 128];
         // ---- the result, or a part of it ----
         bool write = true;
         float* parts = p.parts + (size_t)blockIdx.x * p.splits * p.m * 128 + 32 * quarter + lane;
         if (p.splits > 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (i < p.m) __stcg(parts + ((size_t)blockIdx.y * p.m + i) * 128, acc[i]);
+                if (i < p.m) __stcg(parts + ((size_t)blockIdx.y * p.m + i) * 128, y[i]);
             named_bar(1, 32 * kScalers);
             if (threadIdx.x == 32 * kFirstScaler) {
                 uint32_t* counter = reinterpret_cast<uint32_t*>(p.ws + ws_counter_off()) + blockIdx.x;
@@ -407,19 +429,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
             write = *last_flag != 0;
             if (write) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = i < p.m ? __ldcg(parts + (size_t)i * 128) : 0.f;
+                for (int i = 0; i < N; ++i) y[i] = i < p.m ? __ldcg(parts + (size_t)i * 128) : 0.f;
                 for (int v = 1; v < p.splits; ++v)
 #pragma unroll
                     for (int i = 0; i < N; ++i)
-                        if (i < p.m) acc[i] += __ldcg(parts + ((size_t)v * p.m + i) * 128);
+                        if (i < p.m) y[i] += __ldcg(parts + ((size_t)v * p.m + i) * 128);
             }
         }
         if (write && ch < p.n_out) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (i < p.m) {
-                    if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = acc[i];
-                    else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(acc[i]);
+                    if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = y[i];
+                    else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(y[i]);
                 }
         }
         }
