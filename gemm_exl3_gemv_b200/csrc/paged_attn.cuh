@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "exl3_cache.h"
+#include "exl3_pipe.cuh"
 #include "exl3_tc.cuh"
 
 namespace exl3 {
@@ -152,32 +153,6 @@ __device__ __forceinline__ int count_tiles(const AttnArgs& a, const AttnPlan& pl
     __syncthreads();
     return total;
 }
-
-// Waits that give up: after the first that runs out the others return at once.
-struct Patience {
-    uint32_t* status;
-    bool alive;
-    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity)
-    {
-        if (!alive) return;
-        alive = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-        if (!alive && (threadIdx.x & 31) == 0) atomicOr(status, kStatusTimeout);
-    }
-};
-
-// Stage and phase of a ring.
-template <int N>
-struct Turn {
-    int at = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next()
-    {
-        if (++at == N) {
-            at = 0;
-            phase ^= 1;
-        }
-    }
-};
 
 // The ring of tiles, and the notes about stretches, in shared memory.
 struct Pipes {

@@ -1,13 +1,16 @@
 // q4.cu -- products with plain 4-bit weights in groups (exl3_q4_gemm), and
 // their packing.
 //
-//     y[i][n] = sum_k x[i][k] (q[k][n] - z[k/g][n]) s[k/g][n],   1..32 rows
+//     y[i][n] = sum_k x[i][k] (q[k][n] - z[k/g][n]) s[k/g][n]
 //
-// The product reads half a byte per weight and does 2 m flops with it, so at
-// few rows the stream of packed words is the bound, if a weight costs less
-// than about three instruction slots (148 SMs x 128 lanes at 1.9 GHz against
-// 13e12 weights a second).  At 17..32 rows the legacy tensor pipe's rate
-// (0.92 mma.m16n8k16 per ns and SM measured) is about as tight a bound.
+// This file's kernel takes up to 8 rows, and up to 24 in groups of 32; q4_tc.cu
+// takes the others (see takes_tc()).  The product reads half a byte per weight
+// and does 2 m flops with it, so at few rows the stream of packed words is the
+// bound, if a weight costs less than about three instruction slots (148 SMs x
+// 128 lanes at 1.9 GHz against 13e12 weights a second).  Measured, the words'
+// and scales' bytes over the time: one row of 5120 x 17408 in groups of 128,
+// 15.0 us (3.1 TB/s), of 5120 x 5120 8.2 us: what a launch and the first bytes
+// take, about 4 us, is the larger part.
 //   * The packed tiles (16 channels x 64 inputs, layout in include/exl3.h) are
 //     the A operand of mma.m16n8k16 in register order: a lane's 128-bit load
 //     is its share of four k-steps, and two fields of a word become an fp16
@@ -448,10 +451,18 @@ struct Q4Plan {
 constexpr int most_rows(int shape) { return shape == 0 ? 2 : 8 * shape; }
 constexpr int least_warps_c(int shape) { return shape == 0 ? 1 : shape == 1 ? 2 : 4; }
 
+// Whether the other kernel takes the product.  It decodes faster and needs no
+// more for 32 rows than for 9, but takes a launch more, 16 rows at least, and
+// has a sum per group to read and scale.  This kernel against it, groups of 128:
+// 8 rows of 5120 x 5120 9.0 and 10.5 us, 12 rows 11.6 and 10.6, 32 rows 17.4 and
+// 11.4; 12 rows of 2048 x 2048 6.8 and 6.3.  Groups of 32: 16 rows of 17408 x
+// 5120 23.0 and 27.6 us, 24 rows 28.4 and 32.8, 32 rows 37.1 and 32.5.
+bool takes_tc(int m, int group) { return m > (group == 32 ? 24 : 8); }
+
 Q4Plan q4_plan(int m, int k_in, int n_out)
 {
     Q4Plan pl;
-    pl.shape = m <= 2 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : m <= 24 ? 3 : 4;
+    pl.shape = m <= 2 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : 3;
     pl.ct = pl.shape == 0 ? 1 : 2;
     const int steps = (k_in / 64 + 1) / 2, tiles = (n_out / 16 + pl.ct - 1) / pl.ct;
     const int warps = 148 * 8 * 2;
@@ -498,30 +509,35 @@ cudaError_t launch_q4_g(const Q4Args& a, const Q4Plan& pl, int group, cudaStream
 
 }  // namespace
 
-#ifndef Q4_TC_FROM
-#define Q4_TC_FROM 9
-#endif
 size_t q4_workspace_bytes(int m, int k_in, int n_out)
 {
-    if (m >= Q4_TC_FROM) return q4_tc_workspace_bytes(m, k_in, n_out);
-    const Q4Plan pl = q4_plan(m, k_in, n_out);
-    if (pl.splits == 1) return ws_data_off();
-    return ws_data_off() + align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256);
+    size_t need = 0;                                         // for every size of groups
+    for (int group = 32; group <= 64; group *= 2) {
+        size_t bytes;
+        if (takes_tc(m, group)) {
+            bytes = q4_tc_workspace_bytes(m, k_in, n_out);
+        } else {
+            const Q4Plan pl = q4_plan(m, k_in, n_out);
+            bytes = ws_data_off();
+            if (pl.splits > 1) bytes += align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256);
+        }
+        if (bytes > need) need = bytes;
+    }
+    return need;
 }
 
 cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,
                            const uint8_t* zero, void* y, int y_fp32, int k_in, int n_out, int group,
                            unsigned char* ws, cudaStream_t stream)
 {
-    if (m >= Q4_TC_FROM) return launch_q4_tc(m, x, packed, scale, zero, y, y_fp32, k_in, n_out, group, ws, stream);
+    if (takes_tc(m, group)) return launch_q4_tc(m, x, packed, scale, zero, y, y_fp32, k_in, n_out, group, ws, stream);
     const Q4Plan pl = q4_plan(m, k_in, n_out);
     const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws};
     switch (pl.shape) {
         case 0: return launch_q4_g<0, 1, 1, 4>(a, pl, group, stream);
         case 1: return launch_q4_g<1, 2, 1, 2>(a, pl, group, stream);
-        case 2: return launch_q4_g<2, 2, 2, 2>(a, pl, group, stream);
-        case 3: return launch_q4_g<3, 2, 3, 1>(a, pl, group, stream);
-        default: return launch_q4_g<4, 2, 4, 1>(a, pl, group, stream);
+        case 2: return launch_q4_t<2, 2, 2, 2, 32>(a, pl, stream);
+        default: return launch_q4_t<3, 2, 3, 1, 32>(a, pl, stream);
     }
 }
 

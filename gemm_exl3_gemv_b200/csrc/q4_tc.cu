@@ -1,5 +1,5 @@
-// q4_tc.cu -- products with plain 4-bit weights in groups (exl3_q4_gemm) on the
-// fifth-generation tensor cores.
+// q4_tc.cu -- products with plain 4-bit weights in groups (exl3_q4_gemm) of more
+// than 8 rows (24 in groups of 32), on the fifth-generation tensor cores.
 //
 //     y[i][n] = sum_k x[i][k] (q[k][n] - z[k/g][n]) s[k/g][n]
 //
@@ -17,23 +17,34 @@
 //   * The order of inputs in an MMA's K is the packed layout's: 16 of 32 inputs,
 //     those of the words 2 j or 2 j + 1.  x is brought into shared memory in
 //     that order, in pieces of four inputs (8 bytes).
-//   * Each group of inputs has its own sum in tensor memory, one of several in
-//     turn.  Four warps read it, a channel a thread, scale it in fp32 and add it
-//     up.  Nothing is rounded below 32 bits before the result.
-// Eight warps bring words, zero points and x by cp.async, several stages ahead,
-// and decode; one warp issues the MMAs.  CTAs that split the inputs are joined
-// in order by the last one to arrive.
+//     A small kernel in front lays it out so, once for all CTAs (by 8-byte copies
+//     of every CTA for itself it took 24.5 us, not 19.2), and a bulk copy brings a
+//     stage.
+//   * Each group of inputs has its own sum in tensor memory.  Scaler warps read
+//     it, a channel a thread, scale it in fp32 and add it up.  Nothing is rounded
+//     below 32 bits before the result.
+// What bounds it is the issue of instructions (1700 a stage, most of them the
+// decoders'), 0.38 us a stage and CTA where memory would give 0.18; below that,
+// about 5 us for the launches, the first bytes and the end.  Two sets of warps
+// take stages in turn, so that one stage's waits are another's work: a wait on a
+// barrier costs 150 clocks even if its phase is over.  32 rows of 5120 x 17408 in
+// groups of 128 take 18.8 us (2.6 TB/s; on the legacy tensor pipe 29.9), 16 rows
+// 17.1 (19.9), 32 rows of 5120 x 5120 11.0 (17.3).
+// CTAs that split the inputs of a block of channels are a cluster; they add up
+// their parts, in order, through each other's shared memory (through memory and
+// the last one to arrive: 15.0 us for 5120 x 5120).
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "exl3_cache.h"
+#include "exl3_pipe.cuh"
 #include "exl3_tc.cuh"
 
-#ifndef Q4_LEAST
-#define Q4_LEAST 3
-#endif
 namespace exl3 {
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 struct Q4TcArgs {
     const uint16_t* x;
@@ -45,7 +56,6 @@ struct Q4TcArgs {
     int splits;
     unsigned char* ws;
     const unsigned char* xt;  // x as the stages want it, in the workspace
-    float* parts;             // partial sums, in the workspace
 };
 
 // Warps: two sets of eight decoders, of four scalers and of one that issues MMAs
@@ -63,11 +73,11 @@ struct Q4Tc {
     static constexpr int kParts = 128 / GROUP;               // groups of a stage
     static constexpr int kRing = 8;                          // stages of x in shared memory
     static constexpr int kA = 4;                             // stages of weights in tensor memory
-    static constexpr int kD = 8;                             // sums of groups in turn
+    static constexpr int kD = 8 / kParts;                    // stages whose groups' sums lie there
     static constexpr int kCols = 512;
     static constexpr int kSums = 64 * kA;                    // first column of the sums
-    static_assert(kSums + kD * N <= kCols);
-    static_assert(kRing % kA == 0 && kA % kSets == 0 && kRing * kParts % kD == 0 && kD % (kSets * kParts) == 0);
+    static_assert(kSums + kD * kParts * N <= kCols);
+    static_assert(kRing % kA == 0 && kA % kSets == 0 && kRing % kD == 0 && kD % kSets == 0);
     static constexpr int kWords = 1024;                      // of a decoder's stage
     static constexpr int kOwnRing = 8;                       // stages of a decoder in shared memory
     static_assert(kSets == 2 && kRing == 8 && kA == 4 && kOwnRing == 8);         // the decoders' loop is written for it
@@ -157,45 +167,6 @@ __device__ __forceinline__ uint32_t lds_byte(uint32_t at)
     return v;
 }
 
-// Waits that give up after 2 s: after the first that runs out the others return
-// at once.  The warp tries once; if that fails, its first lane waits, asleep:
-// twenty warps that poll would take the issue slots of the others.
-struct Patience {
-    uint32_t* status;
-    bool alive;
-    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity)
-    {
-        if (!alive || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
-        int there = 1;
-        if ((threadIdx.x & 31) == 0) {
-            const uint64_t t0 = global_ns();
-            while (!mbar_try_wait_sleep(bar, parity, 1000))
-                if (global_ns() - t0 > 2000000000ull) {
-                    there = 0;
-                    atomicOr(status, kStatusTimeout);
-                    break;
-                }
-        }
-        alive = __shfl_sync(0xffffffffu, there, 0) != 0;
-    }
-};
-
-// Place and phase in a ring.
-template <int SIZE>
-struct Turn {
-    int at = 0;
-    uint32_t phase = 0;
-    template <int BY = 1>                                    // a divisor of SIZE
-    __device__ __forceinline__ void next()
-    {
-        at += BY;
-        if (at >= SIZE) {
-            at -= SIZE;
-            phase ^= 1;
-        }
-    }
-};
-
 template <int N, int GROUP>
 __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_constant__ Q4TcArgs p)
 {
@@ -207,26 +178,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     unsigned char* scales = zero_all + S::kZeros;
     uint64_t* full = reinterpret_cast<uint64_t*>(scales + S::kScales);
     uint64_t* done = full + S::kRing;                        // a stage's weights and x are there; its MMAs are done
-    uint64_t* d_full = done + S::kRing;                      // a group's sum is there (a stage's last: done); is read
-    uint64_t* d_empty = d_full + S::kD;
-    uint64_t* all_done = d_empty + S::kD;
+    uint64_t* read = done + S::kRing;                        // a stage's sums are read
+    uint64_t* all_done = read + S::kD;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(all_done + 1);
-    int* last_flag = reinterpret_cast<int*>(tmem_base + 1);
-    static_assert((2 * S::kRing + 2 * S::kD + 1) * 8 + 8 <= 512);
+    static_assert((2 * S::kRing + S::kD + 1) * 8 + 4 <= 512);
 
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
     const int kt_all = p.k_in / 64, stages = (kt_all + 1) / 2;
-    const int s0 = (int)((long long)stages * blockIdx.y / p.splits), s1 = (int)((long long)stages * (blockIdx.y + 1) / p.splits);
+    const int s0 = (int)((long long)stages * blockIdx.x / p.splits), s1 = (int)((long long)stages * (blockIdx.x + 1) / p.splits);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kRing; ++i) {
             mbar_init(full + i, kDecoders + 1);
             mbar_init(done + i, 1);
         }
-        for (int i = 0; i < S::kD; ++i) {
-            mbar_init(d_full + i, 1);
-            mbar_init(d_empty + i, kScalers);
-        }
+        for (int i = 0; i < S::kD; ++i) mbar_init(read + i, kScalers);
         mbar_init(all_done, kSets);
         fence_mbar_init();
     }
@@ -246,10 +212,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
 
     if (warp < kFirstScaler) {
         // ------------------------------------------------------ decoders ---
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 16 warps give up 16 registers a thread, 8 take 32
         // Unrolled over four stages of the set, one round of the ring of stages: what
         // a stage costs beside its arithmetic is most of these warps' instructions.
         const int set = warp / kDecoders, quarter = warp & 3, half = (warp >> 2) & 1;   // of the 128 lanes; of a quarter's 32
-        const int tn_all = p.n_out / 16, tn = min((int)blockIdx.x * 8 + 2 * quarter + half, tn_all - 1);
+        const int tn_all = p.n_out / 16, tn = min((int)blockIdx.y * 8 + 2 * quarter + half, tn_all - 1);
         const int first = s0 + set, s_whole = kt_all / 2;    // k_in may end on half a stage
         const uint32_t own = smem_u32(own_all) + warp * (S::kOwnRing * S::kWords) + lane * 16;
         const uint4* words = reinterpret_cast<const uint4*>(p.packed) + ((long long)tn * kt_all + 2 * first) * 32 + lane;
@@ -339,7 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         }
     } else if (warp < kBringer) {
         // ------------------------------------------------------- scalers ---
-        const int set = (warp - kFirstScaler) / kScalers, quarter = warp & 3, ch0 = blockIdx.x * 128 + 32 * quarter, ch = ch0 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int set = (warp - kFirstScaler) / kScalers, quarter = warp & 3, ch0 = blockIdx.y * 128 + 32 * quarter, ch = ch0 + lane;
         const int first = s0 + set, groups = p.k_in / GROUP;
         // Scales: a copy of the warp brings the 64 bytes of eight groups, eight groups ahead.
         const uint32_t ring = smem_u32(scales) + (warp - kFirstScaler) * (kScaleRing * 64);
@@ -361,7 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) acc[i] = make_float2(0.f, 0.f);
         Turn<S::kRing> here;
-        Turn<S::kD / kParts> d;                              // a stage's sums
+        Turn<S::kD> d;
         here.at = d.at = set;
         uint32_t at = 2 * lane;
         for (int s = first; s < s1; s += kSets) {
@@ -370,28 +338,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
                 __syncwarp();                                // every lane has read the eight before, whose place is the next copy's
                 fetch();
             }
+            float sc[kParts];
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
-                const int gr = s * kParts + part;
-                if (gr >= groups) break;
                 uint16_t sh;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sh) : "r"(ring + at + 64 * part));
-                const float sc = __half2float(__ushort_as_half(sh));
-                const int sum = d.at * kParts + part;
-                if (part == kParts - 1 || gr == groups - 1) wait.wait(done + here.at, here.phase);
-                else wait.wait(d_full + sum, d.phase);
-                tc_fence_after();
-                uint32_t r[N / 16][16];
-#pragma unroll
-                for (int c = 0; c < N / 16; ++c) tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + S::kSums + sum * N + 16 * c, r[c]);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(d_empty + sum);
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i)
-                    fma2(acc[i], make_float2(__uint_as_float(r[i / 8][2 * i % 16]), __uint_as_float(r[i / 8][2 * i % 16 + 1])), make_float2(sc, sc));
+                sc[part] = __half2float(__ushort_as_half(sh));
             }
+            wait.wait(done + here.at, here.phase);
+            tc_fence_after();
+            const uint32_t sums = tmem + ((uint32_t)(32 * quarter) << 16) + S::kSums + d.at * (kParts * N);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                if (s * kParts + part >= groups) break;
+#pragma unroll
+                for (int c = 0; c < N; c += 16) {            // (all at once would take more registers than there are)
+                    uint32_t r[16];
+                    tmem_ld16(sums + part * N + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        fma2(acc[c / 2 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                             make_float2(sc[part], sc[part]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(read + d.at);
             at = (at + 64 * kParts) % (kScaleRing * 64);
             here.template next<kSets>();
             d.template next<kSets>();
@@ -411,32 +384,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) + mine[i * 128];
         // ---- the result, or a part of it ----
-        bool write = true;
-        float* parts = p.parts + (size_t)blockIdx.x * p.splits * p.m * 128 + 32 * quarter + lane;
         if (p.splits > 1) {
+            float* part = reinterpret_cast<float*>(own_all) + 32 * quarter + lane;           // where the first set's decoders had their ring
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < p.m) __stcg(parts + ((size_t)blockIdx.y * p.m + i) * 128, y[i]);
-            named_bar(1, 32 * kScalers);
-            if (threadIdx.x == 32 * kFirstScaler) {
-                uint32_t* counter = reinterpret_cast<uint32_t*>(p.ws + ws_counter_off()) + blockIdx.x;
-                __threadfence();
-                *last_flag = atomicAdd(counter, 1u) == (uint32_t)p.splits - 1;
-                if (*last_flag) *counter = 0;
-                __threadfence();
-            }
-            named_bar(1, 32 * kScalers);
-            write = *last_flag != 0;
-            if (write) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) y[i] = i < p.m ? __ldcg(parts + (size_t)i * 128) : 0.f;
-                for (int v = 1; v < p.splits; ++v)
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (i < p.m) y[i] += __ldcg(parts + ((size_t)v * p.m + i) * 128);
-            }
-        }
-        if (write && ch < p.n_out) {
+            for (int i = 0; i < N; ++i) part[i * 128] = y[i];
+        } else if (ch < p.n_out) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (i < p.m) {
@@ -448,34 +400,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     } else {
         // ----------------------------------------------------- MMA warps ---
         // Unrolled over the ring, so that addresses are a base and constants: what
-        // these warps execute is the longest chain of a stage (two of them took the
-        // 32-row case from @ to @ us).
+        // one of these warps executes is the longest chain of a stage.
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);     // f32 += f16 x f16, both K-major
         const int set = warp - kFirstIssuer;
         const uint64_t x0 = sdesc_sw128(smem_u32(smem) + set * kXStage<N>, 16, 1024);
-        const uint32_t a0 = tmem + 64 * set, sum0 = set * kParts, d0 = tmem + S::kSums + sum0 * N;
+        const uint32_t a0 = tmem + 64 * set, d0 = tmem + S::kSums + set * (kParts * N);
         uint32_t round = 0;                                  // of the ring: its parity is the barriers' phase
         for (int base = s0 + set; base < s1 && wait.alive; base += S::kRing, ++round) {
 #pragma unroll
             for (int i = 0; i < S::kRing; i += kSets) {
                 if (base + i >= s1) break;
                 const bool whole = 2 * (base + i) + 1 < kt_all;
+                wait.wait(read + set + i % S::kD, (round * (S::kRing / S::kD) + i / S::kD + 1) & 1);
                 wait.wait(full + set + i, round & 1);
+                tc_fence_after();
+                if (!wait.alive) break;
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    if (part * GROUP >= 64 && !whole) break;
-                    const int sum = (i * kParts + part) % S::kD;
-                    wait.wait(d_empty + sum0 + sum, (round * (S::kRing * kParts / S::kD) + i * kParts / S::kD + 1) & 1);
-                    tc_fence_after();
-                    if (!wait.alive) break;
-#pragma unroll
-                    for (int k = part * GROUP; k < (part + 1) * GROUP; k += 32)
-                        if (k < 64 || whole)
-                            mma_f16_ts_pair_elect(d0 + sum * N, a0 + 64 * (i % S::kA) + k / 2,
-                                                  x0 + (i * kXStage<N> + (k >> 6) * (N * 128) + 2 * (k & 63)) / 16, idesc, k > part * GROUP);
-                    if (part < kParts - 1) mma_commit_elect(d_full + sum0 + sum);
-                }
-                if (wait.alive) mma_commit_elect(done + set + i);
+                for (int k = 0; k < 128; k += 32)
+                    if (k < 64 || whole)
+                        mma_f16_ts_pair_elect(d0 + (i % S::kD * kParts + k / GROUP) * N, a0 + 64 * (i % S::kA) + k / 2,
+                                              x0 + (i * kXStage<N> + (k >> 6) * (N * 128) + 2 * (k & 63)) / 16, idesc, k % GROUP != 0);
+                mma_commit_elect(done + set + i);
             }
         }
         mma_commit_elect(all_done);                          // before tensor memory is given back
@@ -487,6 +432,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     if (warp == kFirstIssuer) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kCols);
+    }
+    if (p.splits > 1) {
+        // the parts of the inputs, in order; each CTA of the cluster adds up some of the rows
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        float* part = reinterpret_cast<float*>(own_all);
+        const int rows = (p.m - (int)blockIdx.x + p.splits - 1) / p.splits;
+        for (int i = threadIdx.x; i < 32 * rows; i += kTcThreads) {
+            const int row = blockIdx.x + i / 32 * p.splits, at = 4 * (i % 32), ch = blockIdx.y * 128 + at;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int v = 0; v < p.splits; ++v) {
+                const float4 o = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, v) + row * 128 + at);
+                sum.x += o.x, sum.y += o.y, sum.z += o.z, sum.w += o.w;
+            }
+            if (ch >= p.n_out) continue;
+            const long long to = (long long)row * p.n_out + ch;
+            if (p.y_fp32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.y) + to) = sum;
+            } else {
+                const __half2 lo = __floats2half2_rn(sum.x, sum.y), hi = __floats2half2_rn(sum.z, sum.w);
+                *reinterpret_cast<uint2*>(static_cast<__half*>(p.y) + to) = make_uint2(h2_bits(lo), h2_bits(hi));
+            }
+        }
+        cluster.sync();                                      // no CTA leaves while its part is read
     }
 }
 
@@ -524,13 +493,20 @@ cudaError_t launch_t(const Q4TcArgs& a, int blocks, cudaStream_t stream)
     const cudaError_t ex = launch_pdl(q4_x_kernel<N>, dim3((unsigned)((a.k_in / 64 * 8 * N + 255) / 256)), dim3(256), 0, stream, a.x,
                                       a.m, a.k_in, const_cast<unsigned char*>(a.xt));
     if (ex != cudaSuccess) return ex;
-    return launch_pdl(kern, dim3((unsigned)blocks, (unsigned)a.splits), dim3(kTcThreads), S::kSmem, stream, a);
-}
-
-template <int N>
-cudaError_t launch_n(const Q4TcArgs& a, int group, int blocks, cudaStream_t stream)
-{
-    return group == 32 ? launch_t<N, 32>(a, blocks, stream) : group == 64 ? launch_t<N, 64>(a, blocks, stream) : launch_t<N, 128>(a, blocks, stream);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)a.splits, (unsigned)blocks);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 struct Q4TcPlan {
@@ -538,30 +514,30 @@ struct Q4TcPlan {
     size_t x_bytes(int m, int k_in) const { return (size_t)(k_in / 64 + 1) / 2 * (m > 16 ? kXStage<32> : kXStage<16>); }
 };
 
+// CTAs that share a block of channels are a cluster, of up to four: larger ones
+// leave more of the GPU's SMs out.
 Q4TcPlan q4_tc_plan(int k_in, int n_out)
 {
     const int blocks = (n_out + 127) / 128, stages = (k_in / 64 + 1) / 2;
-    int splits = 148 / blocks;
-    if (splits > (stages + Q4_LEAST - 1) / Q4_LEAST) splits = (stages + Q4_LEAST - 1) / Q4_LEAST;
-    return Q4TcPlan{blocks, splits < 1 ? 1 : splits};
+    const int splits = 148 / blocks < 4 ? 148 / blocks : 4;
+    return Q4TcPlan{blocks, splits < 1 ? 1 : splits > stages ? stages : splits};
 }
 
 }  // namespace
 
 size_t q4_tc_workspace_bytes(int m, int k_in, int n_out)
 {
-    const Q4TcPlan pl = q4_tc_plan(k_in, n_out);
-    return ws_data_off() + pl.x_bytes(m, k_in) + (pl.splits == 1 ? 0 : align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * m * 128, 256));
+    return ws_data_off() + q4_tc_plan(k_in, n_out).x_bytes(m, k_in);
 }
 
 cudaError_t launch_q4_tc(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale, const uint8_t* zero,
                          void* y, int y_fp32, int k_in, int n_out, int group, unsigned char* ws, cudaStream_t stream)
 {
     const Q4TcPlan pl = q4_tc_plan(k_in, n_out);
-    unsigned char* xt = ws + ws_data_off();
-    const Q4TcArgs a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws, xt,
-                        reinterpret_cast<float*>(xt + pl.x_bytes(m, k_in))};
-    return m > 16 ? launch_n<32>(a, group, pl.blocks, stream) : launch_n<16>(a, group, pl.blocks, stream);
+    const Q4TcArgs a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws, ws + ws_data_off()};
+    if (m <= 16) return group == 64 ? launch_t<16, 64>(a, pl.blocks, stream) : launch_t<16, 128>(a, pl.blocks, stream);
+    return group == 32 ? launch_t<32, 32>(a, pl.blocks, stream)
+                       : group == 64 ? launch_t<32, 64>(a, pl.blocks, stream) : launch_t<32, 128>(a, pl.blocks, stream);
 }
 
 }  // namespace exl3

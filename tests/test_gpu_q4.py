@@ -146,6 +146,49 @@ def test_q4_repeatable_and_shares_a_workspace(ex, m):
         assert all(torch.equal(a, b) for a, b in zip(ys, first))
 
 
+@pytest.mark.parametrize("m", [2, 13, 31])
+def test_q4_chained_products(ex, m):
+    """A product's rows are another's inputs, right behind the packing of its weights; in a graph too."""
+    import torch
+    a, b = make(m, 1024, 640, 128, seed=20), make(m, 640, 208, 64, seed=21)
+    dev = [{k: torch.from_numpy(v).cuda() for k, v in c.items() if isinstance(v, np.ndarray)} for c in (a, b)]
+    ws = [ex.q4_alloc_workspace(m, 1024, 640), ex.q4_alloc_workspace(m, 640, 208)]
+
+    def run():
+        y = ex.q4_gemm(dev[0]["x"], ex.q4_pack(dev[0]["q"]), dev[0]["scale"], dev[0]["zero"], 128, workspace=ws[0])
+        return y, ex.q4_gemm(y, ex.q4_pack(dev[1]["q"]), dev[1]["scale"], dev[1]["zero"], 64, fp32=True, workspace=ws[1])
+
+    def check(y, z):
+        close(y, *reference(a), False)
+        close(z, *reference({**b, "x": y.cpu().numpy()}), True)
+
+    check(*run())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for _ in range(2):
+        dev[0]["x"].mul_(0.5)
+        a["x"] = dev[0]["x"].cpu().numpy()
+        g.replay()
+        check(*out)
+
+
+@pytest.mark.parametrize("m,k,group", [(12, 640, 64), (32, 5120, 128)])
+def test_q4_withheld_inputs_time_out_and_report(ex, m, k, group):
+    """x withheld through the workspace's injection word: the waits run out, the call ends and the status
+    says so; the next call is right."""
+    import torch
+    c = make(m, k, 256, group, seed=22)
+    d = {k: torch.from_numpy(v).cuda() for k, v in c.items() if isinstance(v, np.ndarray)}
+    packed, ws = ex.q4_pack(d["q"]), ex.q4_alloc_workspace(m, k, 256)
+    ws[4:8] = 1
+    ex.q4_gemm(d["x"], packed, d["scale"], d["zero"], group, workspace=ws)
+    assert ex.workspace_status(ws) == ex.EXL3_ERR_TIMEOUT
+    ws[4:8] = 0
+    close(ex.q4_gemm(d["x"], packed, d["scale"], d["zero"], group, fp32=True, workspace=ws), *reference(c), True)
+    assert ex.workspace_status(ws) == ex.EXL3_OK
+
+
 def test_q4_refusals(ex):
     import torch
     c = make(2, 128, 32, 64, seed=8)
