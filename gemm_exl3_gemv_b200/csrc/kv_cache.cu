@@ -208,30 +208,37 @@ __global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n,
     }
     // ---- the bookkeeping ----
     __syncthreads();                                         // every thread has read the list of copies
-    // the lowest `total` free pages are taken: which entry's page is each?
-    int rank = free_before, e = -1;
-    for (int w = w0; w < w1 && rank < total; ++w) {
-        uint32_t bits = __ldcg(a.free + w), take = 0;
-        for (; bits && rank < total; bits &= bits - 1, ++rank) {
-            const int page = 32 * w + __ffs(bits) - 1;
-            if (e < 0) {                                     // the last entry that begins at or in front of this rank
-                e = 0;
-                int hi = n;
+    // The lowest `total` free pages are taken: which entry's page is each?  A warp
+    // takes its threads' words one after the other, a page a lane.
+    const int lane = tid & 31;
+    int rank = free_before;
+    for (int i = 0; i < wper; ++i) {
+        const int w = w0 + i;
+        const uint32_t mine = w < w1 && rank < total ? __ldcg(a.free + w) : 0;
+        uint32_t todo = __ballot_sync(0xffffffffu, mine != 0);
+        for (; todo; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1, word = __shfl_sync(0xffffffffu, w, from);
+            const uint32_t bits = __shfl_sync(0xffffffffu, mine, from);
+            const int r = __shfl_sync(0xffffffffu, rank, from) + __popc(bits & ((1u << lane) - 1));
+            const bool taken = (bits >> lane & 1) && r < total;
+            if (taken) {
+                int e = 0, hi = n;                           // the last entry that begins at or in front of this rank
                 while (hi - e > 1) {
                     const int mid = (e + hi) / 2;
-                    (ahead[mid] <= rank ? e : hi) = mid;
+                    (ahead[mid] <= r ? e : hi) = mid;
                 }
+                const int page = 32 * word + lane;
+                a.refs[page] = 1;
+                const int s = seqs[e], c = counts ? counts[e] : m, len = a.lens[s];
+                const int fresh = pages_of(len + c, ps) - pages_of(len, ps), nth = r - ahead[e];
+                const bool copied_too = ahead[e + 1] - ahead[e] > fresh;
+                if (copied_too && nth == 0) copies[e] = page;    // (the list of copies is done with)
+                else a.table[(long long)s * a.max_pages + pages_of(len, ps) + nth - copied_too] = page;
             }
-            while (rank >= ahead[e + 1]) ++e;
-            take |= bits & -bits;
-            a.refs[page] = 1;
-            const int s = seqs[e], c = counts ? counts[e] : m, len = a.lens[s];
-            const int fresh = pages_of(len + c, ps) - pages_of(len, ps), nth = rank - ahead[e];
-            const bool copied_too = ahead[e + 1] - ahead[e] > fresh;
-            if (copied_too && nth == 0) copies[e] = page;    // (the list of copies is done with)
-            else a.table[(long long)s * a.max_pages + pages_of(len, ps) + nth - copied_too] = page;
+            const uint32_t all = __ballot_sync(0xffffffffu, taken);
+            if (lane == 0 && all) atomicAnd(a.free + word, ~all);
         }
-        if (take) atomicAnd(a.free + w, ~take);
+        rank += __popc(mine);
     }
     __syncthreads();                                         // the free bits and the old lengths were read
 #pragma unroll
@@ -247,10 +254,13 @@ __global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n,
 }
 
 // ------------------------------------------------------------------ write ---
-// A thread moves 16 bytes of a key and of a value.  Bound by memory; what the
-// places cost (sequence, length, page: three dependent loads) is shared by the
-// 16 pieces of a row through the L1.  Every CTA checks the whole list first, as
-// a repeated sequence would be written by two entries in no order.
+// grid.y: the list's entries.  A thread moves 16 bytes of a key and of a value
+// at a time; what the places cost (sequence, length, page: three dependent
+// loads) is shared by the pieces of a row through the L1.  Every CTA checks the
+// whole list first, as a repeated sequence would be written by two entries in
+// no order.  Bound by memory: 2001 tokens of two sequences, 8 heads of 128, take
+// 7.4 us (4.4 TB/s); of one token of 64 sequences, 2.3 us, the launch and the
+// chain of reads.
 
 __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int n, int m, const int* seqs, const int* counts,
                                                        const uint16_t* k_new, const uint16_t* v_new, long long bs,
@@ -260,30 +270,36 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int 
     for (int i = threadIdx.x; i < (a.n_seqs + 31) / 32; i += blockDim.x) seen[i] = 0;
     grid_dep_wait();
     grid_dep_launch();
+    const int b = blockIdx.y, s = seqs[b], c = counts ? counts[b] : m;
     const int old_fault = __ldcg(a.scratch + kKvFault);
     __syncthreads();
     bool bad = false;
     for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, seqs[e], a.n_seqs) || (counts && counts[e] > m);
     if (__syncthreads_or(bad)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) fault(a, kKvIndex);
+        if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) fault(a, kKvIndex);
         return;
     }
     if (old_fault) return;
-    const int row_vec = a.n_heads * a.head_dim / 8, head_vec = a.head_dim / 8, ps = a.page_size;
-    const long long all = (long long)n * m * row_vec;
-    const long long page_el = (long long)a.n_heads * ps * a.head_dim;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (long long)gridDim.x * blockDim.x) {
-        const int vec = (int)(i % row_vec);
-        const long long r = i / row_vec;
-        const int b = (int)(r / m), row = (int)(r % m);
-        const int c = counts ? counts[b] : m, s = seqs[b];
-        if (row >= c) continue;
-        const int pos = a.lens[s] - c + row;
-        if (pos < 0 || pos >= a.max_pages * ps) { fault(a, kKvIndex); continue; }
-        const int page = a.table[(long long)s * a.max_pages + pos / ps];
+    const int row_vec = a.n_heads * a.head_dim / 8, head_vec = a.head_dim / 8, shift = __ffs(a.page_size) - 1;
+    const long long page_el = (long long)a.n_heads * a.page_size * a.head_dim;
+    const int* pages = a.table + (long long)s * a.max_pages;
+    const int first = a.lens[s] - c;
+    // this thread's places in the entry's rows
+    const uint32_t at = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+    int row = (int)(at / row_vec), vec = (int)(at % row_vec);
+    const int row_step = (int)(step / row_vec), vec_step = (int)(step % row_vec);
+    for (; row < c; row += row_step, vec += vec_step) {
+        if (vec >= row_vec) {
+            vec -= row_vec;
+            if (++row >= c) break;
+        }
+        const int pos = first + row;
+        if (pos < 0 || pos >= a.max_pages << shift) { fault(a, kKvIndex); continue; }
+        const int page = pages[pos >> shift];
         if (!page_ok(a, page)) { fault(a, kKvIndex); continue; }
+        const int head = vec / head_vec;
         const long long to = ((long long)layer * a.n_pages + page) * page_el +
-                             ((long long)(vec / head_vec) * ps + pos % ps) * a.head_dim + 8 * (vec % head_vec);
+                             ((((long long)head << shift) + (pos & (a.page_size - 1))) * a.head_dim + 8 * (vec - head * head_vec));
         const long long from = b * bs + row * rs + 8 * vec;
         *reinterpret_cast<uint4*>(a.k + to) = *reinterpret_cast<const uint4*>(k_new + from);
         *reinterpret_cast<uint4*>(a.v + to) = *reinterpret_cast<const uint4*>(v_new + from);
@@ -519,8 +535,8 @@ cudaError_t launch_kv_write(const KvArgs& a, int layer, int n, int m, const int*
                             const uint16_t* k_new, const uint16_t* v_new, long long batch_stride,
                             long long row_stride, cudaStream_t stream)
 {
-    const long long pieces = (long long)n * m * a.n_heads * a.head_dim / 8, blocks = (pieces + 255) / 256;
-    return launch_pdl(kv_write_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)), dim3(256), seen_bytes(a),
+    const long long blocks = ((long long)m * a.n_heads * a.head_dim / 8 + 255) / 256, most = 148 * 8 / n + 1;
+    return launch_pdl(kv_write_kernel, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)n), dim3(256), seen_bytes(a),
                       stream, a, layer, n, m, seqs, counts, k_new, v_new, batch_stride, row_stride);
 }
 
