@@ -17,9 +17,9 @@
 //   * The order of inputs in an MMA's K is the packed layout's: 16 of 32 inputs,
 //     those of the words 2 j or 2 j + 1.  x is brought into shared memory in
 //     that order, in pieces of four inputs (8 bytes).
-//     A small kernel in front lays it out so, once for all CTAs (by 8-byte copies
-//     of every CTA for itself it took 24.5 us, not 19.2), and a bulk copy brings a
-//     stage.
+//     A small kernel in front lays it out so, once for all CTAs, and a bulk copy
+//     brings a stage.  (Copies of 8 bytes by every CTA for itself kept four warps
+//     busy, 32 requests a stage.)
 //   * Each group of inputs has its own sum in tensor memory.  Scaler warps read
 //     it, a channel a thread, scale it in fp32 and add it up.  Nothing is rounded
 //     below 32 bits before the result.

@@ -31,7 +31,6 @@ import torch
 from . import exl3 as ex
 
 MAX_LIST = 1024         # entries of a list of sequences
-MAX_ROWS = 32           # new tokens per sequence of one attention call
 
 _F16, _I32 = torch.float16, torch.int32
 _extend, _write, _truncate = ex.lib.exl3_kv_extend, ex.lib.exl3_kv_write, ex.lib.exl3_kv_truncate

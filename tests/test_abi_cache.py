@@ -161,7 +161,7 @@ def test_tensor_checks_without_a_gpu(ex):
     """The binding refuses tensors of the wrong place before it calls the library."""
     import torch
     if torch.cuda.is_available():
-        pytest.skip("host tensors are refused on a GPU box by the GPU tests")
+        pytest.skip("where there is a GPU the GPU tests cover it")
     x = torch.zeros(1, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
         ex.q4_gemm(x, torch.zeros(1, 1, 32, 4, dtype=torch.int32), torch.zeros(1, 16, dtype=torch.float16), group=64)
