@@ -422,7 +422,7 @@ extern "C" int exl3_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, co
         return EXL3_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(packed) || !aligned16(scale) || !aligned16(zero) || !aligned16(y))
         return EXL3_ERR_MISALIGNED;
-    if (!workspace || ws_bytes < exl3_q4_workspace_bytes(m, k_in, n_out)) return EXL3_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < exl3::q4_workspace_need(m, k_in, n_out, group)) return EXL3_ERR_WORKSPACE;
     if (!aligned256(workspace)) return EXL3_ERR_MISALIGNED;
     const int st = check_arch();
     if (st != EXL3_OK) return st;

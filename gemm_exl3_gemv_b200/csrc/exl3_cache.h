@@ -25,7 +25,8 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
 }
 
 // Products with plain 4-bit weights (q4.cu).
-size_t q4_workspace_bytes(int m, int k_in, int n_out);
+size_t q4_workspace_need(int m, int k_in, int n_out, int group);
+size_t q4_workspace_bytes(int m, int k_in, int n_out);        // for up to m rows, whatever the groups
 cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,
                            const uint8_t* zero, void* y, int y_fp32, int k_in, int n_out, int group,
                            unsigned char* ws, cudaStream_t stream);

@@ -512,21 +512,22 @@ cudaError_t launch_q4_g(const Q4Args& a, const Q4Plan& pl, int group, cudaStream
 
 }  // namespace
 
+size_t q4_workspace_need(int m, int k_in, int n_out, int group)
+{
+    if (takes_tc(m, group)) return q4_tc_workspace_bytes(m, k_in, n_out);
+    const Q4Plan pl = q4_plan(m, k_in, n_out);
+    return ws_data_off() + (pl.splits == 1 ? 0 : align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256));
+}
+
 size_t q4_workspace_bytes(int m, int k_in, int n_out)
 {
-    size_t need = 0;                                         // for every size of groups
-    for (int group = 32; group <= 64; group *= 2) {
-        size_t bytes;
-        if (takes_tc(m, group)) {
-            bytes = q4_tc_workspace_bytes(m, k_in, n_out);
-        } else {
-            const Q4Plan pl = q4_plan(m, k_in, n_out);
-            bytes = ws_data_off();
-            if (pl.splits > 1) bytes += align_up(sizeof(float) * (size_t)pl.blocks * pl.splits * 16 * pl.ct * pl.warps_c * m, 256);
+    size_t most = 0;
+    for (int rows = 1; rows <= m; ++rows)
+        for (int group = 32; group <= 64; group *= 2) {      // (128 as 64)
+            const size_t need = q4_workspace_need(rows, k_in, n_out, group);
+            if (need > most) most = need;
         }
-        if (bytes > need) need = bytes;
-    }
-    return need;
+    return most;
 }
 
 cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, const uint16_t* scale,

@@ -318,7 +318,7 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  *   group  : 32, 64 or 128.   k_in : positive multiple of 64 and of group, at
  *            most 2^20.   n_out : positive multiple of 16, at most 1,048,576.
  *   workspace, ws_bytes : at least exl3_q4_workspace_bytes(m, k_in, n_out)
- *            bytes, 256-byte aligned, zero-filled before first use; shared by
+ *            bytes (which is enough for fewer rows too), 256-byte aligned, zero-filled before first use; shared by
  *            calls on one stream as described at exl3_workspace_bytes (it may
  *            be the same buffer as the trellis products').
  * Layout of packed: tiles of 16 channels x 64 inputs, tile (tn, tk) at
@@ -326,7 +326,7 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  *   (g < 8, t < 4, j < 4) holds channels 16*tn + g + 8*c, c < 2, and inputs
  *   64*tk + 32*(j/2) + 8*t + 4*(j%2) + i, i < 4, each value at bit
  *   4*c + 8*(i/2) + 16*(i%2).
- * The weights enter the tensor cores as exact integers q - zero, products are
+ * The weights enter the tensor cores exactly, as integers; products are
  * summed in fp32, and each group's sum is scaled in fp32.  The order of every
  * sum is fixed: repeated calls are bitwise identical.  An infinity or NaN in a
  * row of x makes outputs of that row infinite or NaN (which of the two depends

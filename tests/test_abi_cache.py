@@ -117,6 +117,9 @@ def test_sizes(ex):
                 (1, 64, (1 << 20) + 16)):
         assert q(*bad) == 0, bad
     assert q(1, 64, 16) > 0 and q(32, 17408, 5120) > 0
+    for shape in ((1024, 4096), (17408, 1024), (2048, 2048), (64, 16), (5120, 33024)):
+        sizes = [q(m, *shape) for m in range(1, 33)]
+        assert sizes == sorted(sizes)                   # enough for fewer rows too
 
 
 def test_q4(ex):

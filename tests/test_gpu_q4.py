@@ -72,6 +72,47 @@ def test_q4_narrow_and_deep(ex, m, group):
         close(on_gpu(ex, c, fp32=True), *reference(c), True)
 
 
+@pytest.mark.parametrize("m,k,n,group", [(9, 192, 33008, 64), (32, 128, 38016, 32), (12, 65536, 16, 128), (32, 64, 2048, 64),
+                                         (25, 4160, 4112, 32), (16, 128, 128, 128)])
+def test_q4_many_rows_extremes(ex, m, k, n, group):
+    """More blocks of channels than the GPU has places, one block of many inputs, one stage of inputs (or half
+    of one), a last block and a last stage that are not full."""
+    c = make(m, k, n, group, seed=m + 3 * group, zero=m != 32)
+    close(on_gpu(ex, c, fp32=True), *reference(c), True)
+
+
+def test_q4_one_workspace_for_any_rows(ex):
+    """The workspace for 32 rows serves every number of rows, one product after the other."""
+    import torch
+    c = make(32, 1024, 4096, 64, seed=23)
+    d = {k: torch.from_numpy(v).cuda() for k, v in c.items() if isinstance(v, np.ndarray)}
+    packed, ws = ex.q4_pack(d["q"]), ex.q4_alloc_workspace(32, 1024, 4096)
+    ref, tol = reference(c)
+    for m in (32, 1, 24, 8, 9, 2, 17, 16, 32):
+        close(ex.q4_gemm(d["x"][:m], packed, d["scale"], d["zero"], 64, fp32=True, workspace=ws), ref[:m], tol[:m], True)
+
+
+def test_q4_side_by_side_on_streams(ex):
+    """Products of all three kernels on streams of their own: each as alone."""
+    import torch
+    cases = [make(32, 2048, 4096, 128, seed=24), make(12, 4096, 1024, 64, seed=25), make(3, 2048, 2048, 32, seed=26)]
+    dev = [{k: torch.from_numpy(v).cuda() for k, v in c.items() if isinstance(v, np.ndarray)} for c in cases]
+    packed = [ex.q4_pack(d["q"]) for d in dev]
+    ws = [ex.q4_alloc_workspace(c["x"].shape[0], *c["q"].shape) for c in cases]
+    call = lambda i: ex.q4_gemm(dev[i]["x"], packed[i], dev[i]["scale"], dev[i]["zero"], cases[i]["group"], fp32=True, workspace=ws[i])
+    alone = [call(i) for i in range(3)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], [[], [], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(i))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        close(alone[i], *reference(c), True)
+        assert all(torch.equal(y, alone[i]) for y in got[i])
+
+
 def test_q4_pack_layout(ex):
     """Every word of the packed tiles, field by field from the documented layout."""
     import torch
