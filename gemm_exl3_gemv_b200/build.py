@@ -1,8 +1,9 @@
-"""Build libexl3.so (sm_100a) in-tree with nvcc.
+"""Build libexl3.so (sm_100a) in-tree with nvcc, and the compiled part of the
+Python binding with the C compiler.
 
     python -m gemm_exl3_gemv_b200.build [--force]
 
-The shared library lands next to this file; the ctypes binding loads it from
+The shared libraries land next to this file; the binding loads them from
 there.  nvcc cross-compiles, so no GPU is needed to build.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -78,8 +80,23 @@ def _compile(lib: str, extra, verbose: bool):
     os.replace(tmp, lib)
 
 
+# the compiled part of the binding: calls that a decode step makes many times
+BINDING, BINDING_SRC = os.path.join(HERE, "_binding.so"), os.path.join(CSRC, "binding.c")
+
+
+def _compile_binding(force: bool):
+    inputs = [BINDING_SRC, os.path.join(ROOT, "include", "exl3.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, inputs)):
+        return
+    tmp = f"{BINDING}.tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+                    "-I", os.path.join(ROOT, "include"), "-o", tmp, BINDING_SRC], check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
     """Build libexl3.so (and, unless debug=False, libexl3_debug.so) if stale."""
+    _compile_binding(force)
     if force or stale(LIB):
         _compile(LIB, [], verbose)
     if debug and (force or stale(LIB_DEBUG)):

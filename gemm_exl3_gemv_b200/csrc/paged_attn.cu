@@ -452,12 +452,12 @@ static_assert(2 * kMaxCtas + 2 <= kMaxBlocks);               // a counter a slot
 
 constexpr int kLeastTiles = 2;                               // of a CTA's share, without the second kernel
 
-// Whether the second kernel joins.  It costs a launch, and about 6 us behind
+// Whether the second kernel joins.  It costs a launch, and about 4 us behind
 // the first; one CTA takes 1 to 3 us for the 2 or 3 parts of an ordinary group
 // of 16 rows (32 sequences of up to 4000 tokens: 64 us, with the second kernel
-// 68), but 20 us for 37 parts (one sequence of 131077 tokens: 117 us, 103), and
-// 10 to 17 us for 6 parts of 80 rows (16 drafted tokens of 8 sequences: 63 us,
-// 53).  Short tables are cut into few parts whatever the rows.
+// 68), but much longer for many parts (one sequence of 8192 tokens 26 us, 18
+// with it; of 131077 106 and 102) or for 6 parts of 80 rows (16 drafted tokens of
+// 8 sequences: 62 us, 46).  Short tables are cut into few parts whatever the rows.
 bool defer_join(const KvArgs& c, int n, int tile_rows)
 {
     const long long tiles = (long long)c.max_pages * c.page_size / kTile + 1;
@@ -509,9 +509,9 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream)
     if ((e = layer_map(kmap, fn, a.c, a.c.k, a.layer)) != cudaSuccess) return e;
     if ((e = layer_map(vmap, fn, a.c, a.c.v, a.layer)) != cudaSuccess) return e;
     // Another CTA for fewer tiles than these costs more in the join than it
-    // saves: one sequence of 8192 tokens takes 20, 17.5 and 18.3 us with 2, 4
-    // and 8, 16 drafted tokens behind it 41, 35 and 32 us; without the second
-    // kernel, one of 100 tokens takes 7, 10 and 16 us.
+    // saves: one sequence of 8192 tokens takes 20, 18 and 18 us with 2, 4 and 8,
+    // 16 drafted tokens behind it 40, 34 and 29 us; without the second kernel, one
+    // of 100 tokens takes 7, 10 and 16 us.
     const bool deferred = defer_join(a.c, a.n, r.tile_rows);
     const int least = !deferred ? kLeastTiles : r.tile_rows > 16 ? 8 : 4;
     const AttnPlan pl = {r.row_tiles, r.tile_rows, a.n * r.row_tiles, __builtin_ctz(a.c.page_size), deferred, least,

@@ -128,6 +128,14 @@ lib.exl3_paged_attention.restype = _I
 lib.exl3_paged_attention_launches.argtypes = [_P, _I, _I, _I]
 lib.exl3_paged_attention_launches.restype = _I
 
+# The same entry points of the same library without ctypes' conversions, which
+# cost a small call up to a quarter of its time (csrc/binding.c).
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError("_binding.so not built; run `python -m gemm_exl3_gemv_b200.build`") from e
+_binding.bind([ctypes.cast(getattr(lib, _name), _P).value for _name in _binding.NAMES])
+
 
 class Exl3Error(RuntimeError):
     def __init__(self, status: int, what: str):
@@ -312,6 +320,7 @@ def gemm_grouped(problems, bits: int, fp32: bool = False, workspace: Optional[to
 # ------------------------------------------------- plain 4-bit weights ---
 
 _F16, _I32, _U8 = torch.float16, torch.int32, torch.uint8
+_q4_gemm = _binding.q4_gemm
 
 
 def _dense(t: torch.Tensor, dtype, shape, device: int) -> bool:
@@ -399,7 +408,7 @@ def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Op
         _expect(out, "out", torch.float32 if fp32 else torch.float16, (m, n_out), device)
     if workspace is None:
         workspace = q4_alloc_workspace(m, k_in, n_out, device=x.device)
-    st = lib.exl3_q4_gemm(m, x2.data_ptr(), packed.data_ptr(), scale.data_ptr(),
+    st = _q4_gemm(m, x2.data_ptr(), packed.data_ptr(), scale.data_ptr(),
                           None if zero is None else zero.data_ptr(), out.data_ptr(), 1 if fp32 else 0, k_in, n_out, group,
                           workspace.data_ptr(), _room(workspace, device),
                           _raw_stream(device) if stream is None else stream.cuda_stream)

@@ -33,8 +33,8 @@ from . import exl3 as ex
 MAX_LIST = 1024         # entries of a list of sequences
 
 _F16, _I32 = torch.float16, torch.int32
-_extend, _write, _truncate = ex.lib.exl3_kv_extend, ex.lib.exl3_kv_write, ex.lib.exl3_kv_truncate
-_fork, _compact, _attention = ex.lib.exl3_kv_fork, ex.lib.exl3_kv_compact, ex.lib.exl3_paged_attention
+_extend, _write, _truncate = ex._binding.kv_extend, ex._binding.kv_write, ex._binding.kv_truncate
+_fork, _compact, _attention = ex._binding.kv_fork, ex._binding.kv_compact, ex._binding.paged_attention
 
 
 class KvCache:
@@ -69,7 +69,7 @@ class KvCache:
         self._desc = ex.Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                               free.data_ptr(), self.scratch.data_ptr(), n_layers, n_pages, n_heads, page_size,
                               head_dim, n_seqs, max_pages)
-        self._ref = ctypes.byref(self._desc)
+        self._ref, self._at = ctypes.byref(self._desc), ctypes.addressof(self._desc)
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, n_heads: int, page_size: int, head_dim: int, n_seqs: int,
@@ -156,7 +156,7 @@ class KvCache:
         n = self._entries(seqs, "seqs")
         p, c, s = self._list(seqs, "seqs", n), self._list(counts, "counts", n), self._where(stream)
         if n:
-            st = _extend(self._ref, n, m, p, c, s)
+            st = _extend(self._at, n, m, p, c, s)
             if st:
                 ex._check(st, "exl3_kv_extend")
 
@@ -171,7 +171,7 @@ class KvCache:
             raise ValueError("k and v must have the same type, device, shape and strides")
         s = self._where(stream)
         if n and m:
-            st = _write(self._ref, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s)
+            st = _write(self._at, layer, n, m, p, c, k.data_ptr(), v.data_ptr(), bs, rs, s)
             if st:
                 ex._check(st, "exl3_kv_write")
 
@@ -180,7 +180,7 @@ class KvCache:
         n = self._entries(seqs, "seqs")
         p, c, s = self._list(seqs, "seqs", n), self._list(lens, "lens", n), self._where(stream)
         if n:
-            st = _truncate(self._ref, n, p, c, s)
+            st = _truncate(self._at, n, p, c, s)
             if st:
                 ex._check(st, "exl3_kv_truncate")
 
@@ -189,13 +189,13 @@ class KvCache:
         n = self._entries(src, "src")
         p, d, s = self._list(src, "src", n), self._list(dst, "dst", n), self._where(stream)
         if n:
-            st = _fork(self._ref, n, p, d, s)
+            st = _fork(self._at, n, p, d, s)
             if st:
                 ex._check(st, "exl3_kv_fork")
 
     def compact(self, stream=None):
         """Moves pages so that the used ones are the first of the pool."""
-        st = _compact(self._ref, self._where(stream))
+        st = _compact(self._at, self._where(stream))
         if st:
             ex._check(st, "exl3_kv_compact")
 
@@ -246,7 +246,7 @@ class KvCache:
             return out
         if workspace is None:
             workspace = self.attention_workspace(n, m, heads)
-        st = _attention(self._ref, layer, n, m, p, c, q.data_ptr(), qb, qr, heads, self._scale if scale is None else scale,
+        st = _attention(self._at, layer, n, m, p, c, q.data_ptr(), qb, qr, heads, self._scale if scale is None else scale,
                         window, sinks, out.data_ptr(), ob, orow, None if lse is None else lse.data_ptr(),
                         workspace.data_ptr(), ex._room(workspace, self._index), s)
         if st:

@@ -155,6 +155,48 @@ def test_attention_launches(ex):
     assert f(c, 0, 1, 8) == f(c, 1025, 1, 8) == f(c, 1, 0, 8) == f(c, 1, 33, 8) == f(c, 1, 1, 6) == f(cache(ex, k=None), 1, 1, 8) == 0
 
 
+def test_compiled_binding(ex):
+    """The compiled calls hand over every argument as ctypes does: the same status whichever argument is wrong.
+    Every call is refused for its last check (no room, a misaligned list or stride) if for nothing before it."""
+    b, desc = ex._binding, cache(ex)._obj
+    at = ctypes.addressof(desc)
+    inv, uns, mis = ex.EXL3_ERR_INVALID_ARG, ex.EXL3_ERR_UNSUPPORTED, ex.EXL3_ERR_MISALIGNED
+    wrong = {                                            # the call; argument: values and what they give
+        "exl3_q4_gemm": ([1, 16, 16, 16, 16, 16, 0, 256, 64, 64, 256, 0, 0],
+                         {0: [(0, inv), (33, uns)], 1: [(None, inv), (18, mis)], 2: [(None, inv), (18, mis)],
+                          3: [(None, inv), (18, mis)], 4: [(17, mis)], 5: [(None, inv), (18, mis)], 7: [(0, inv), (96, uns)],
+                          8: [(0, inv), (24, uns)], 9: [(48, uns)]}),
+        "exl3_kv_extend": ([at, 1, 1, 17, 16, 0], {0: [(None, inv)], 1: [(0, inv), (1025, uns)], 2: [(0, inv)], 3: [(None, inv)]}),
+        "exl3_kv_write": ([at, 0, 1, 1, 16, 16, 16, 16, 4, 4, 0],
+                          {0: [(None, inv)], 1: [(-1, inv), (2, inv)], 2: [(0, inv), (1025, uns)], 3: [(0, inv)], 4: [(None, inv)],
+                           6: [(None, inv)], 7: [(None, inv)], 8: [(-8, inv)], 9: [(-8, inv)]}),
+        "exl3_kv_truncate": ([at, 1, 17, 16, 0], {0: [(None, inv)], 1: [(0, inv), (1025, uns)], 2: [(None, inv)]}),
+        "exl3_kv_fork": ([at, 1, 16, 17, 0], {0: [(None, inv)], 1: [(0, inv), (1025, uns)], 2: [(None, inv)], 3: [(None, inv)]}),
+        "exl3_kv_compact": ([None, 0], {}),
+        "exl3_paged_attention": ([at, 0, 1, 2, 16, 16, 16, 64, 64, 8, 1.0, 0, 0, 16, 1024, 1024, 16, 256, 0, 0],
+                                 {0: [(None, inv)], 1: [(2, inv)], 2: [(0, inv), (1025, uns)], 3: [(0, inv), (33, uns)], 4: [(None, inv)],
+                                  5: [(3, mis)], 6: [(None, inv), (24, mis)], 7: [(-8, inv), (4, mis)], 8: [(-8, inv), (4, mis)],
+                                  9: [(0, inv), (6, uns)], 10: [(float("inf"), inv)], 11: [(-1, inv)], 12: [(-1, inv)],
+                                  13: [(None, inv), (24, mis)], 14: [(-8, inv), (4, mis)], 15: [(-8, inv), (1016, inv), (1028, mis)],
+                                  16: [(20, mis)]}),
+    }
+    assert set(wrong) == set(b.NAMES)
+    for name, (args, changes) in wrong.items():
+        call, reference = getattr(b, name[len("exl3_"):]), getattr(ex.lib, name)
+        base = call(*args)
+        assert base == reference(*args) != ex.EXL3_OK
+        for i, values in changes.items():
+            for value, status in values:
+                one = args[:i] + [value] + args[i + 1:]
+                assert call(*one) == reference(*one) == status, (name, i, value)
+        with pytest.raises(TypeError):
+            call(*args[:-1])
+        with pytest.raises(TypeError):
+            call(*args[:-1], "0")
+    with pytest.raises(OverflowError):
+        b.kv_extend(at, 1 << 40, 1, 17, None, 0)
+
+
 def test_status_strings(ex):
     assert b"CACHE_FULL" in ex.lib.exl3_status_string(ex.EXL3_ERR_CACHE_FULL)
     assert b"INDEX" in ex.lib.exl3_status_string(ex.EXL3_ERR_INDEX)
