@@ -506,15 +506,20 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_small_kernel(KvArg
     int border;
     const int moves = pair_pages<kMoveThreads>(a, src, dst, tmp, border);
     if (moves == 0) return;                                  // the same in every CTA
+    // counted in as one that has read the free bits; whether it was the last one is asked for behind the moves
+    int before = 0;
     if (threadIdx.x == 0) {
         __threadfence();
-        is_last = atomicAdd(a.scratch + kKvArrived, 1) == (int)gridDim.x - 1;
+        before = atomicAdd(a.scratch + kKvArrived, 1);
+    }
+    move_pages(a, src, dst, moves, border);
+    if (threadIdx.x == 0) {
+        is_last = before == (int)gridDim.x - 1;
         if (is_last) a.scratch[kKvArrived] = 0;
         __threadfence();
     }
     __syncthreads();
     if (is_last) free_behind(a, border, threadIdx.x, kMoveThreads);
-    move_pages(a, src, dst, moves, border);
 }
 
 size_t seen_bytes(const KvArgs& a) { return sizeof(uint32_t) * (size_t)((a.n_seqs + 31) / 32); }
