@@ -360,6 +360,9 @@ def q4_alloc_workspace(m: int, k_in: int, n_out: int, device=None) -> torch.Tens
 def q4_pack(q: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """4-bit values (k_in, n_out) uint8 in the layout of ``q4_gemm``:
     (n_out/16, k_in/64, 32, 4) int32.  Once per matrix, when it is loaded."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):                 # what is allocated here belongs to the stream that uses it
+            return q4_pack(q)
     if q.dim() != 2:
         raise ValueError("q: expected (k_in, n_out)")
     k_in, n_out = q.shape
@@ -379,6 +382,9 @@ def q4_gemm(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: Op
     for x of shape (m, k_in), m <= 32, or (k_in,).  packed: from ``q4_pack``;
     scale: (k_in / group, n_out) fp16; zero: the same in uint8 (0..15), None
     for 8 everywhere.  Inference only: there is no backward pass."""
+    if stream is not None and (out is None or workspace is None):
+        with torch.cuda.stream(stream):                 # what is allocated here belongs to the stream that uses it
+            return q4_gemm(x, packed, scale, zero, group, out, fp32, workspace)
     squeeze = x.dim() == 1
     x2 = x.reshape(1, -1) if squeeze else x
     device = x.get_device()

@@ -41,7 +41,8 @@ class KvCache:
     """k, v: (n_layers, n_pages, n_heads, page_size, head_dim) fp16; table:
     (n_seqs, max_pages) int32; lens: (n_seqs,) int32; refs: (n_pages,) int32;
     free: (ceil(n_pages / 32),) int32 bits.  The cache takes the tensors as
-    they are (``KvCache.empty`` makes and clears them)."""
+    they are (``KvCache.empty`` makes and clears them); its scratch memory is
+    cleared on the current stream."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                  refs: torch.Tensor, free: torch.Tensor):
@@ -75,11 +76,14 @@ class KvCache:
     def empty(cls, n_layers: int, n_pages: int, n_heads: int, page_size: int, head_dim: int, n_seqs: int,
               max_pages: int, device=None, stream=None) -> "KvCache":
         """An empty cache with memory of its own (zero-filled keys and values)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):             # what is allocated here belongs to the stream that uses it
+                return cls.empty(n_layers, n_pages, n_heads, page_size, head_dim, n_seqs, max_pages, device)
         device = device or "cuda"
         pool = lambda: torch.zeros((n_layers, n_pages, n_heads, page_size, head_dim), dtype=torch.float16, device=device)
         words = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
         cache = cls(pool(), pool(), words(n_seqs, max_pages), words(n_seqs), words(n_pages), words((n_pages + 31) // 32))
-        cache.reset(stream)
+        cache.reset()
         return cache
 
     # ------------------------------------------------------------ checks ---
@@ -226,6 +230,9 @@ class KvCache:
         default.  lse: (n, m, n_q_heads) fp32, filled with the logarithms of
         the softmax sums.  Rows from counts[b] on are left as they were (in an
         ``out`` made here: zero)."""
+        if stream is not None and (out is None or workspace is None):
+            with torch.cuda.stream(stream):             # what is allocated here belongs to the stream that uses it
+                return self.attention(layer, seqs, q, counts, scale, window, sinks, out, lse, workspace)
         n = self._entries(seqs, "seqs")
         p, c = self._list(seqs, "seqs", n), self._list(counts, "counts", n)
         heads = q.shape[2] if q.dim() == 4 else 0

@@ -101,3 +101,36 @@ def test_serving_steps():
     cache.check()
     assert cache.lens.tolist() == [len(tokens[s][0][0]) for s in range(6)]
     assert ex.workspace_status(ws) == ex.EXL3_OK
+
+
+def test_a_stream_given_gets_its_own_memory():
+    """Calls on a stream that is given, with the results, workspaces and the cache made by the calls, while the
+    current stream is busy and memory that is handed out again holds ones."""
+    import torch
+    from gemm_exl3_gemv_b200 import exl3 as ex
+    from gemm_exl3_gemv_b200.kvcache import KvCache
+    rng = np.random.default_rng(31)
+    dev = lambda a: torch.from_numpy(a).cuda()
+    x, q = rng.standard_normal((12, 2048)).astype(np.float16), rng.integers(0, 16, (2048, 128)).astype(np.uint8)
+    scale = rng.uniform(0.01, 0.02, (32, 128)).astype(np.float16)
+    k, v, qq = (rng.standard_normal((1, 600 if i < 2 else 4, 2, 128)).astype(np.float16) for i in range(3))
+    gx, gq, gs, gk, gv, gqq, ids = dev(x), dev(q), dev(scale), dev(k), dev(v), dev(qq), torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        ones = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in (1 << 16, 1 << 20, 1 << 22)]
+    torch.cuda.synchronize()
+    del ones
+    torch.cuda._sleep(100_000_000)                        # some 50 ms of the current stream
+    c = KvCache.empty(1, 16, 2, 64, 128, 1, 12, stream=stream)
+    c.extend(ids, 600, stream=stream)
+    c.write(0, ids, gk, gv, stream=stream)
+    att = c.attention(0, ids, gqq, stream=stream)
+    ys = [ex.q4_gemm(gx[:m], ex.q4_pack(gq, stream=stream), gs, None, 64, fp32=True, stream=stream) for m in (1, 12)]
+    stream.synchronize()
+    got, gys = att.double().cpu().numpy()[0], [y.double().cpu().numpy() for y in ys]
+    assert c.status(stream) == ex.EXL3_OK
+    w = (q.astype(np.float64) - 8) * np.repeat(scale.astype(np.float64), 64, 0)
+    for m, y in zip((1, 12), gys):                        # 2048 inputs in fp32: 152 steps of 2^-22 of the magnitudes
+        assert np.all(np.abs(y - x[:m].astype(np.float64) @ w) <= 152 * 2.0 ** -22 * (np.abs(x[:m].astype(np.float64)) @ np.abs(w)))
+    ref, _, tol, _ = cache_model.attention(qq[0].astype(np.float64), k[0].astype(np.float64), v[0].astype(np.float64), 596, 128 ** -0.5)
+    assert np.all(np.abs(got - ref) <= tol)
