@@ -14,14 +14,11 @@
 //   * The packed tiles (16 channels x 64 inputs, layout in include/exl3.h) are
 //     the A operand of mma.m16n8k16 in register order: a lane's 128-bit load
 //     is its share of four k-steps, and two fields of a word become an fp16
-//     pair by one AND with a mask.
-//     Up to 8 rows the masked fields are the operand: as fp16 bits they are
-//     the subnormals q 2^-24 (fields at bits 0 and 16) and q 2^-20 (bits 4 and
-//     20), which the tensor cores take exactly; the zero point is taken off
-//     the group's sum, with sum(x) from one more mma of ones.
-//     For more rows the zero point is taken off the operand, (q - z) in
-//     integers below 2048, exact in fp16: that costs four packed adds a word,
-//     and saves the mma of ones and the second FMA of every sum.
+//     pair by one AND-OR and one packed add: (q - z), an integer below 2048,
+//     exact in fp16.  (Taking z sum(x) off the group's sum instead, with the
+//     fields as they are, cancels where q is near z: a channel of q = z came
+//     out as rounding errors of sum(q x) and not as zero.  It is no faster: one
+//     row of 5120 x 17408 12.8 us and 12.9 so, of 17408 x 5120 17.1 and 16.8.)
 //   * Words, scales, zero points and x come by asynchronous copies through
 //     rings in shared memory: a warp's own for the weights, one shared by the
 //     warps that work on the same inputs for x, whose B fragments are 128-bit
@@ -86,25 +83,16 @@ __device__ __forceinline__ __half2 masked_1024(uint32_t w, uint32_t mask)
     return bits_h2(r);
 }
 
-// The A fragment of one k-step: rows g (a0, a2) and g + 8 (a1, a3) of the tile.
-// RAW: the fields as subnormals, 2^-24 and 2^-20 of their values.  Otherwise
+// The A fragment of one k-step: rows g (a0, a2) and g + 8 (a1, a3) of the tile,
 // q - z from 1024 + q and 1024 + 16 q: zlo = -(1024 + z), zhi = -(64 + z).
-template <bool RAW>
 __device__ __forceinline__ void q4_fragment(uint32_t w, __half2 zlo, __half2 zhi, uint32_t (&a)[4])
 {
     const uint32_t v = w >> 8;
-    if constexpr (RAW) {
-        a[0] = w & 0x000F000Fu;
-        a[1] = w & 0x00F000F0u;
-        a[2] = v & 0x000F000Fu;
-        a[3] = v & 0x00F000F0u;
-    } else {
-        const __half2 sixteenth = __float2half2_rn(0.0625f);
-        a[0] = h2_bits(__hadd2(masked_1024(w, 0x000F000Fu), zlo));
-        a[1] = h2_bits(__hfma2(masked_1024(w, 0x00F000F0u), sixteenth, zhi));
-        a[2] = h2_bits(__hadd2(masked_1024(v, 0x000F000Fu), zlo));
-        a[3] = h2_bits(__hfma2(masked_1024(v, 0x00F000F0u), sixteenth, zhi));
-    }
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    a[0] = h2_bits(__hadd2(masked_1024(w, 0x000F000Fu), zlo));
+    a[1] = h2_bits(__hfma2(masked_1024(w, 0x00F000F0u), sixteenth, zhi));
+    a[2] = h2_bits(__hadd2(masked_1024(v, 0x000F000Fu), zlo));
+    a[3] = h2_bits(__hfma2(masked_1024(v, 0x00F000F0u), sixteenth, zhi));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
@@ -160,7 +148,6 @@ template <int CT, int NT, int SPS, int GROUP>
 __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) q4_gemm_kernel(const __grid_constant__ Q4Args p)
 {
     using S = Q4Shape<CT, NT, SPS, GROUP>;
-    constexpr bool kRaw = NT == 1;
     constexpr int kParts = S::kParts;
     extern __shared__ __align__(128) unsigned char smem[];
     float* red = reinterpret_cast<float*>(smem);             // after the loop: inputs' warps x rows x channels
@@ -261,7 +248,7 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
 #pragma unroll
     for (int n = 0; n < NT; ++n) row_at[n] = min(8 * n + g, p.m - 1) * S::kXRow + 16 * t;
 
-    float sum[CT][NT][4], xs[4];
+    float sum[CT][NT][4];
     __half2 zlo[CT], zhi[CT];
     // 64 inputs (the first or second tile of a step) from shared memory
     auto tile = [&](auto second, uint32_t words_at, const uint32_t (&x_at)[NT], uint32_t scales, uint32_t zeros) {
@@ -273,7 +260,7 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
         for (int half = 0; half < 2; ++half) {               // 32 inputs
             const int k = 64 * kSecond + 32 * half, part = k / GROUP;
             const bool opens = k % GROUP == 0, closes = (k + 32) % GROUP == 0;
-            if (!kRaw && opens) {
+            if (opens) {
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     const int ch = (part * CT + c) * 16;
@@ -290,7 +277,7 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     uint32_t a[4];
-                    q4_fragment<kRaw>(half ? (i ? w[c].w : w[c].z) : (i ? w[c].y : w[c].x), zlo[c], zhi[c], a);
+                    q4_fragment(half ? (i ? w[c].w : w[c].z) : (i ? w[c].y : w[c].x), zlo[c], zhi[c], a);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint32_t b0 = i ? x[n].z : x[n].x, b1 = i ? x[n].w : x[n].y;
@@ -298,27 +285,12 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
                         else mma_16816(sum[c][n], a, b0, b1);
                     }
                 }
-                if constexpr (kRaw) {
-                    const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-                    const uint32_t b0 = i ? x[0].z : x[0].x, b1 = i ? x[0].w : x[0].y;
-                    if (opens && i == 0) mma_16816_first(xs, ones, b0, b1);
-                    else mma_16816(xs, ones, b0, b1);
-                }
             }
             if (closes) {
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     const int ch = (part * CT + c) * 16;
-                    float s_lo = lds_half(scales + 2 * ch), s_hi = lds_half(scales + 2 * ch + 16);
-                    if constexpr (kRaw) {
-                        // a byte in the last places of 2^23, less 2^23
-                        const float z_lo = (__uint_as_float(0x4B000000u | lds_byte(zeros + ch)) - 8388608.f) * 0x1p-24f;
-                        const float z_hi = (__uint_as_float(0x4B000000u | lds_byte(zeros + ch + 8)) - 8388608.f) * 0x1p-20f;
-                        s_lo *= 0x1p24f;
-                        s_hi *= 0x1p20f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[c][0][e] -= (e < 2 ? z_lo : z_hi) * xs[e];
-                    }
+                    const float s_lo = lds_half(scales + 2 * ch), s_hi = lds_half(scales + 2 * ch + 16);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -329,10 +329,10 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  * The weights enter the tensor cores exactly, as integers; products are
  * summed in fp32, and each group's sum is scaled in fp32.  The order of every
  * sum is fixed: repeated calls are bitwise identical.  An infinity or NaN in a
- * row of x makes outputs of that row infinite or NaN (which of the two depends
- * on m: up to 8 rows the zero point is taken off the group's sum), and touches
- * no other row.  Timeouts, where m > 8: as in exl3_gemm_small_m (reported by
- * exl3_workspace_status alone; a nonzero injection word withholds x).
+ * row of x makes outputs of that row what the definition gives (infinite, or
+ * NaN where q = zero), and touches no other row.  Timeouts, where m > 8: as in
+ * exl3_gemm_small_m (reported by exl3_workspace_status alone; a nonzero
+ * injection word withholds x).
  */
 EXL3_API size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out);
 EXL3_API int exl3_q4_gemm(int m, const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
