@@ -45,4 +45,21 @@ struct Patience {
     }
 };
 
+// A named barrier over `threads` threads that tells each of them whether any of
+// them said yes: the same answer for all, with nothing in shared memory that a
+// faster warp could write over.
+__device__ __forceinline__ bool named_bar_any(int id, int threads, bool yes)
+{
+    int any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"(yes ? 1 : 0)
+        : "memory");
+    return any != 0;
+}
+
 }  // namespace exl3

@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
     uint64_t* q_full = heard + 2;
     uint64_t* q_empty = q_full + 1;
     Stretch* notes = reinterpret_cast<Stretch*>(q_empty + 1);
-    int* flags = reinterpret_cast<int*>(notes + 2);          // last to arrive; a wait of the consumers has run out
-    static_assert((2 * S::kStages + 6) * 8 + 2 * sizeof(Stretch) + 8 <= 512);
+    int& last = *reinterpret_cast<int*>(notes + 2);          // whether this CTA is a group's last to arrive
+    static_assert((2 * S::kStages + 6) * 8 + 2 * sizeof(Stretch) + 4 <= 512);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
         mbar_init(q_full, 1);
         mbar_init(q_empty, S::kWarps);
         fence_mbar_init();
-        flags[1] = 0;
     }
     grid_dep_wait();
     grid_dep_launch();
@@ -122,10 +121,10 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
     const Pipes io = {smem, full, empty, told, heard, notes};
     uint32_t q_phase = 0;
     if (warp == S::kWarps) {
-        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [&](const Stretch& st) {
+        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [&](const Stretch& st, bool withhold) {
             p.wait(q_empty, q_phase ^ 1);
             q_phase ^= 1;
-            if (!p.alive) return;
+            if (!p.alive || withhold) return;
             if (lane == 0) mbar_arrive_expect_tx(q_full, st.en.rows * 2 * D);
             __syncwarp();
             if (lane < st.en.rows) {                         // row by row
@@ -146,9 +145,9 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
     Turn<2> note;
     while (true) {
         p.wait(told + note.at, note.phase);
-        if (!p.alive && lane == 0) flags[1] = 1;
-        everyone();
-        if (flags[1]) return;                                // all of them: none waits for another at a barrier
+        // where a wait of one of the warps has run out all of them leave: none waits for another at a barrier, and how
+        // many barriers lie behind this one depends on the note alone
+        if (named_bar_any(1, S::kConsumers, !p.alive)) return;
         const Stretch st = notes[note.at];
         __syncwarp();
         if (lane == 0) mbar_arrive(heard + note.at);
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
                     __stcg(reinterpret_cast<float2*>(at + wt * CPW + 8 * d + 2 * t), make_float2(o[d][2 * i], o[d][2 * i + 1]));
                 if (t == 0 && wt == 0) __stcg(reinterpret_cast<float2*>(at + D), make_float2(mx[i], sum[i]));
             }
-            hand_in<S, D>(a, pl, cut, st, flags[0], tid);
+            hand_in<S, D>(a, pl, cut, st, last, tid);
         }
     }
 }

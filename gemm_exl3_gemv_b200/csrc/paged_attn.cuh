@@ -165,8 +165,12 @@ struct Pipes {
 // The producer warp: walks the CTA's range, tells what the stretches are and
 // brings their tiles (TMA, one box per page part and 64 columns, 128-byte
 // swizzle).  Its reads of lengths and tables run ahead of the work: with the
-// memory saturated, each dependent read takes 2 us.  queries(stretch, its
-// entry): called once per stretch, before its tiles.
+// memory saturated, each dependent read takes 2 us.  queries(stretch, withhold):
+// called once per stretch, before its tiles.
+// A note is written only after the consumers of the one before have said that
+// they read it; where that or any other wait runs out, the warp leaves and the
+// consumers' own waits run out.  So a note never changes under its readers, and
+// all warps of a CTA take the same stretches.
 template <int D, int STAGES, int THREADS, typename Queries>
 __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const CUtensorMap* kmap,
                                         const CUtensorMap* vmap, const int* front, const Pipes& io, Patience& p, Queries queries)
@@ -176,7 +180,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
     Turn<STAGES> stage;
     Turn<2> note;
     // a nonzero injection word (tests of the timeout path) withholds every copy
-    p.alive = *reinterpret_cast<const volatile uint32_t*>(a.ws + kWsInjectOff) == 0u;
+    const bool withhold = *reinterpret_cast<const volatile uint32_t*>(a.ws + kWsInjectOff) != 0u;
     int u = cut.first(blockIdx.x);
     const int u1 = cut.first(blockIdx.x + 1);
     // the entry that tile u belongs to: of the last thread whose entries begin at or in front of it
@@ -194,6 +198,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
         const int h = (u - base) / en.tiles, off = (u - base) - h * en.tiles;
         const int n = min(en.tiles - off, u1 - u), b = e / pl.row_tiles;
         p.wait(io.heard + note.at, note.phase ^ 1);
+        if (!p.alive) return;
         const Stretch st = {en, b, h, n, off, u - off, first};
         if (lane == 0) {
             io.notes[note.at] = st;
@@ -201,7 +206,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
         }
         __syncwarp();
         note.next();
-        queries(st);
+        queries(st, withhold);
         const int* row = a.c.table + (long long)en.seq * a.c.max_pages;
         const int held = (en.len + ps - 1) >> pl.page_shift;
         for (int i0 = 0; i0 < n; i0 += 32 / parts) {
@@ -222,12 +227,12 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
             const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
             for (int k = 0; k < 32 / parts && i0 + k < n; ++k) {
                 p.wait(io.empty + stage.at, stage.phase ^ 1);
-                if (!p.alive) continue;                      // no more copies; the consumers give up as well
+                if (!p.alive) return;
                 const uint32_t mask = (good >> (k * parts)) & ((1u << parts) - 1);
                 unsigned char* kt = io.ring + stage.at * 2 * kHalf;
-                if (lane == 0) mbar_arrive_expect_tx(io.full + stage.at, __popc(mask) * part_rows * D * 4);
+                if (lane == 0 && !withhold) mbar_arrive_expect_tx(io.full + stage.at, __popc(mask) * part_rows * D * 4);
                 __syncwarp();
-                if (lane / parts == k && page >= 0) {
+                if (lane / parts == k && page >= 0 && !withhold) {
                     const int y = ((page * heads + h) << pl.page_shift) + (token & (ps - 1));
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x) {
@@ -243,6 +248,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
         u += n;
     }
     p.wait(io.heard + note.at, note.phase ^ 1);
+    if (!p.alive) return;
     if (lane == 0) {
         io.notes[note.at].en.rows = 0;
         io.notes[note.at].n = 0;

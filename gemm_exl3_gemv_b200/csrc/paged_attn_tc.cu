@@ -116,11 +116,10 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
     uint64_t* q_full = pv_done + 1;
     uint64_t* all_done = q_full + 1;
     Stretch* notes = reinterpret_cast<Stretch*>(all_done + 1);
-    // last to arrive; a wait of the softmax warps has run out; tile that holds values that are not finite (by parity);
-    // tile whose stretch's O begins with them
+    // whether this CTA is a group's last to arrive; tile whose stretch's O begins with values that are not finite
     int* flags = reinterpret_cast<int*>(notes + 2);
-    uint32_t* tmem_base = reinterpret_cast<uint32_t*>(flags + 5);
-    static_assert((2 * S::kStages + 12) * 8 + 2 * sizeof(Stretch) + 24 <= 512);
+    uint32_t* tmem_base = reinterpret_cast<uint32_t*>(flags + 2);
+    static_assert((2 * S::kStages + 12) * 8 + 2 * sizeof(Stretch) + 12 <= 512);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
         mbar_init(q_full, 4);
         mbar_init(all_done, 1);
         fence_mbar_init();
-        flags[1] = flags[2] = flags[3] = flags[4] = 0;
+        flags[1] = 0;
     }
     grid_dep_wait();
     grid_dep_launch();
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
     const Pipes io = {smem, full, empty, told, heard, notes};
 
     if (warp == 4) {
-        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [](const Stretch&) {});
+        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [](const Stretch&, bool) {});
     } else if (warp == 5) {
         // ------------------------------------------------------ MMA warp ---
         constexpr uint32_t id_qk = idesc_f16(128, kTile, false), id_pv = idesc_f16(128, D, true);
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
             if (p.alive) {
                 tc_fence_after();
                 const uint32_t pt = smem_u32(p_smem), vt = smem_u32(smem + done.at * 2 * S::kHalf) + S::kHalf;
-                const bool fresh = first && *reinterpret_cast<volatile int*>(flags + 4) != tile;
+                const bool fresh = first && *reinterpret_cast<volatile int*>(flags + 1) != tile;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
                     mma_f16_ss_elect(tmem_o, sdesc_sw128(pt + 32 * k, 16, 1024), sdesc_sw128(vt + 2048 * k, kTile * 128, 1024),
@@ -237,9 +236,9 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
         };
         while (true) {
             p.wait(told + note.at, note.phase);
-            if (!p.alive && lane == 0) flags[1] = 1;
-            everyone();
-            if (flags[1]) break;                             // all of them: none waits for another at a barrier
+            // where a wait of one of the warps has run out all of them leave: none waits for another at a barrier, and
+            // how many barriers lie behind this one depends on the note, and on answers that all of them get
+            if (named_bar_any(1, S::kConsumers, !p.alive)) break;
             const Stretch st = notes[note.at];
             __syncwarp();
             if (lane == 0) mbar_arrive(heard + note.at);
@@ -301,9 +300,8 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
                     for (int j = 0; j < kTile; ++j) s[j] = j < hi && (j >= lo || j < sk) ? s[j] : kNegInf;
                     // values: what no row of the tile sees is cleared; is there anything that is not finite?
                     p.wait(full + stage.at, stage.phase);
-                    wait_products(tile - 1);                 // every warp has read the flag of two tiles ago
                     bool odd = false;
-#pragma unroll 2
+#pragma unroll 1                                             // two at a time, 128 columns spill: 16 drafted of 8 x 8192 49.7 us, 45.7 so
                     for (int i = tid; i < kTile * (D / 8); i += S::kConsumers) {
                         const int r = i / (D / 8);
                         const uint32_t at = vt + swizzled(kTile, r, i % (D / 8));
@@ -311,9 +309,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
                         if (!any_sees(tok0 + r)) sts16(at, make_uint4(0, 0, 0, 0));
                         else odd |= (finite_halves(v.x) & finite_halves(v.y) & finite_halves(v.z) & finite_halves(v.w)) != 0xffffffffu;
                     }
-                    if (odd) flags[2 + (tile & 1)] = tile + 1;
-                    everyone();
-                    odd_values = flags[2 + (tile & 1)] == tile + 1;
+                    odd_values = named_bar_any(1, S::kConsumers, odd);
                 }
                 stage.next();
 
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(ShapeTc<D>::kThreads, 2)
                         tmem_st16(tmem_o + lanes + c, o);
                     }
                     tmem_st_wait();
-                    if (it == 0) flags[4] = tile + 1;
+                    if (it == 0) flags[1] = tile + 1;
                     everyone();
                     for (int i = tid; i < kTile * (D / 8); i += S::kConsumers) {
                         const uint32_t at = vt + swizzled(kTile, i / (D / 8), i % (D / 8));
