@@ -45,6 +45,17 @@ struct Patience {
     }
 };
 
+// Waits, with the same limit, for the last of `issued` copies that a warp sent
+// round a ring, copy i to place i % SIZE, whose barrier's phase they complete:
+// none is on its way to a CTA's shared memory when the CTA ends, whichever
+// waits ran out.
+template <int SIZE>
+__device__ __forceinline__ void copies_landed(uint64_t* bars, int issued, uint32_t* status)
+{
+    Patience p = {status, true};
+    for (int i = max(0, issued - SIZE); i < issued; ++i) p.wait(bars + i % SIZE, (uint32_t)(i / SIZE) & 1u);
+}
+
 // A named barrier over `threads` threads that tells each of them whether any of
 // them said yes: the same answer for all, with nothing in shared memory that a
 // faster warp could write over.

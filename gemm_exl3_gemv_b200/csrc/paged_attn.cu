@@ -121,10 +121,12 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
     const Pipes io = {smem, full, empty, told, heard, notes};
     uint32_t q_phase = 0;
     if (warp == S::kWarps) {
-        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [&](const Stretch& st, bool withhold) {
+        int asked = 0;                                       // stretches whose queries were sent for
+        produce<D, S::kStages, S::kThreads>(a, pl, cut, &kmap, &vmap, front, io, p, [&](const Stretch& st, bool allowed) {
             p.wait(q_empty, q_phase ^ 1);
             q_phase ^= 1;
-            if (!p.alive || withhold) return;
+            if (!p.alive || !allowed) return;
+            ++asked;
             if (lane == 0) mbar_arrive_expect_tx(q_full, st.en.rows * 2 * D);
             __syncwarp();
             if (lane < st.en.rows) {                         // row by row
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(Shape16<D>::kThreads, 2)
                          a.q + st.b * a.q_bs + tok * a.q_rs + (long long)(st.h * a.group + rr - tok * a.group) * D, 2 * D, q_full);
             }
         });
+        copies_landed<1>(q_full, asked, p.status);
         return;
     }
 

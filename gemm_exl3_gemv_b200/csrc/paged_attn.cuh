@@ -165,22 +165,26 @@ struct Pipes {
 // The producer warp: walks the CTA's range, tells what the stretches are and
 // brings their tiles (TMA, one box per page part and 64 columns, 128-byte
 // swizzle).  Its reads of lengths and tables run ahead of the work: with the
-// memory saturated, each dependent read takes 2 us.  queries(stretch, withhold):
+// memory saturated, each dependent read takes 2 us.  queries(stretch, allowed):
 // called once per stretch, before its tiles.
 // A note is written only after the consumers of the one before have said that
 // they read it; where that or any other wait runs out, the warp leaves and the
 // consumers' own waits run out.  So a note never changes under its readers, and
-// all warps of a CTA take the same stretches.
+// all warps of a CTA take the same stretches.  `issued` counts the tiles that it
+// sent for.
 template <int D, int STAGES, int THREADS, typename Queries>
-__device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const CUtensorMap* kmap,
-                                        const CUtensorMap* vmap, const int* front, const Pipes& io, Patience& p, Queries queries)
+__device__ __forceinline__ void walk(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const CUtensorMap* kmap,
+                                        const CUtensorMap* vmap, const int* front, const Pipes& io, Patience& p, Queries queries,
+                                     int& issued)
 {
     constexpr int kHalf = kTile * D * 2;                     // bytes of a tile's keys (or values)
     const int lane = threadIdx.x & 31, heads = a.c.n_heads, per = (pl.entries + THREADS - 1) / THREADS;
     Turn<STAGES> stage;
     Turn<2> note;
-    // a nonzero injection word (tests of the timeout path) withholds every copy
-    const bool withhold = *reinterpret_cast<const volatile uint32_t*>(a.ws + kWsInjectOff) != 0u;
+    // a nonzero injection word, low byte v (tests of the timeout path), lets the first v - 1 tiles through and withholds
+    // the others (and the queries of a stretch that begins behind them)
+    const uint32_t inject = *reinterpret_cast<const volatile uint32_t*>(a.ws + kWsInjectOff);
+    const int most = inject ? max((int)(inject & 255u) - 1, 0) : 0x7fffffff;
     int u = cut.first(blockIdx.x);
     const int u1 = cut.first(blockIdx.x + 1);
     // the entry that tile u belongs to: of the last thread whose entries begin at or in front of it
@@ -206,7 +210,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
         }
         __syncwarp();
         note.next();
-        queries(st, withhold);
+        queries(st, issued < most);
         const int* row = a.c.table + (long long)en.seq * a.c.max_pages;
         const int held = (en.len + ps - 1) >> pl.page_shift;
         for (int i0 = 0; i0 < n; i0 += 32 / parts) {
@@ -228,11 +232,12 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
             for (int k = 0; k < 32 / parts && i0 + k < n; ++k) {
                 p.wait(io.empty + stage.at, stage.phase ^ 1);
                 if (!p.alive) return;
+                const bool allowed = issued < most;
                 const uint32_t mask = (good >> (k * parts)) & ((1u << parts) - 1);
                 unsigned char* kt = io.ring + stage.at * 2 * kHalf;
-                if (lane == 0 && !withhold) mbar_arrive_expect_tx(io.full + stage.at, __popc(mask) * part_rows * D * 4);
+                if (lane == 0 && allowed) mbar_arrive_expect_tx(io.full + stage.at, __popc(mask) * part_rows * D * 4);
                 __syncwarp();
-                if (lane / parts == k && page >= 0 && !withhold) {
+                if (lane / parts == k && page >= 0 && allowed) {
                     const int y = ((page * heads + h) << pl.page_shift) + (token & (ps - 1));
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x) {
@@ -243,6 +248,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
                 }
                 __syncwarp();
                 stage.next();
+                issued += allowed;
             }
         }
         u += n;
@@ -254,6 +260,16 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, c
         io.notes[note.at].n = 0;
         mbar_arrive(io.told + note.at);
     }
+}
+
+// The producer warp's part of the kernel.
+template <int D, int STAGES, int THREADS, typename Queries>
+__device__ __forceinline__ void produce(const AttnArgs& a, const AttnPlan& pl, const AttnCut& cut, const CUtensorMap* kmap,
+                                        const CUtensorMap* vmap, const int* front, const Pipes& io, Patience& p, Queries queries)
+{
+    int issued = 0;
+    walk<D, STAGES, THREADS>(a, pl, cut, kmap, vmap, front, io, p, queries, issued);
+    copies_landed<STAGES>(io.full, issued, p.status);
 }
 
 // Counts the calling CTA in; true in the last of `of` CTAs, which may then read

@@ -291,10 +291,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     } else if (warp == kBringer) {
         // ------------------------------------------------------------- x ---
         grid_dep_wait();                                     // the kernel before lays x out
-        // a nonzero injection word (tests of the timeout path) withholds every copy
-        const bool withhold = *reinterpret_cast<const volatile uint32_t*>(p.ws + kWsInjectOff) != 0u;
+        // a nonzero injection word, low byte v (tests of the timeout path), lets the first v - 1 copies through
+        const uint32_t inject = *reinterpret_cast<const volatile uint32_t*>(p.ws + kWsInjectOff);
+        const int most = inject ? max((int)(inject & 255u) - 1, 0) : 0x7fffffff;
         Turn<S::kRing> slot;
-        for (int s = s0; s < s1 && !withhold; ++s) {
+        int issued = 0;
+        for (int s = s0; s < s1 && issued < most; ++s, ++issued) {
             wait.wait(done + slot.at, slot.phase ^ 1);
             if (!wait.alive) break;
             if (lane == 0) {
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
             __syncwarp();
             slot.next();
         }
+        copies_landed<S::kRing>(full, issued, wait.status);
     } else if (warp < kBringer) {
         // ------------------------------------------------------- scalers ---
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");

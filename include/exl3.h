@@ -332,7 +332,7 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  * row of x makes outputs of that row what the definition gives (infinite, or
  * NaN where q = zero), and touches no other row.  Timeouts, where m > 8: as in
  * exl3_gemm_small_m (reported by exl3_workspace_status alone; a nonzero
- * injection word withholds x).
+ * injection word, low byte v, lets a CTA's first v - 1 stages of x through).
  */
 EXL3_API size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out);
 EXL3_API int exl3_q4_gemm(int m, const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
@@ -482,9 +482,10 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  * A table entry out of range is not followed: exl3_kv_status then reports
  * EXL3_ERR_INDEX, and the rows that needed it are not valid; the same for a
  * bad number in seqs, whose rows are left as they were.  Bounded waits as in
- * exl3_gemm_small_m (exl3_workspace_status; its injection word withholds every
- * copy here too).  After EXL3_ERR_TIMEOUT, zero-fill the workspace before its
- * next use: parts of a cut sequence may have been counted and not joined.
+ * exl3_gemm_small_m (exl3_workspace_status; a nonzero injection word, low byte
+ * v, lets a CTA's first v - 1 tiles through).  After EXL3_ERR_TIMEOUT, zero-fill
+ * the workspace before its next use: parts of a cut sequence may have been
+ * counted and not joined.
  */
 EXL3_API size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
 /* Kernel launches of one call (0 for an invalid one).  Host-only. */

@@ -47,3 +47,18 @@ def test_cut_sequences_with_a_second_kernel(ex, m):
     ws.zero_()
     c.check(c.run(workspace=ws))
     assert ex.workspace_status(ws) == ex.EXL3_OK
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("m,group", [(1, 4), (6, 4)])        # both kernels
+@pytest.mark.parametrize("v", [2, 8])
+def test_some_tiles_come_and_the_others_do_not(ex, m, group, v, dim):
+    """The first v - 1 tiles of each CTA arrive, so that products are done and stages in use when a wait runs out."""
+    c = Case([64 * 70 * 9, 1000, 64 * 70 * 5], [m] * 3, kv_heads=4, group=group, dim=dim, page=64, m=m, seed=v)
+    ws = c.cache.attention_workspace(3, m, 4 * group)
+    ws[4:8] = c.torch.tensor([v, 0, 0, 0], dtype=c.torch.uint8)
+    c.run(workspace=ws)
+    assert ex.workspace_status(ws) == ex.EXL3_ERR_TIMEOUT
+    ws.zero_()
+    c.check(c.run(workspace=ws))
+    assert ex.workspace_status(ws) == ex.EXL3_OK
