@@ -357,7 +357,7 @@ EXL3_API int exl3_q4_pack(const uint8_t *q, int k_in, int n_out, uint32_t *packe
  *            t % page_size of each head.  A page id stands for that page of
  *            every layer.
  *   table  : n_seqs x max_pages int32: the page ids of each sequence, in
- *            order; -1 behind the last.
+ *            order; -1 behind the last (what stands there does not matter).
  *   lens   : n_seqs int32: tokens of each sequence (0: it holds nothing).
  *   refs   : n_pages int32: how many sequences hold each page.
  *   free   : ceil(n_pages / 32) uint32: bit p % 32 of word p / 32 is set while
