@@ -128,13 +128,44 @@ lib.exl3_paged_attention.restype = _I
 lib.exl3_paged_attention_launches.argtypes = [_P, _I, _I, _I]
 lib.exl3_paged_attention_launches.restype = _I
 
+
+class _CtypesBinding:
+    """The calls of csrc/binding.c through ctypes, with its checks of the
+    arguments' number and types: 1 to 3 us slower a call, and needs no compiler."""
+    NAMES = ("exl3_q4_gemm", "exl3_kv_extend", "exl3_kv_write", "exl3_kv_truncate", "exl3_kv_fork", "exl3_kv_compact",
+             "exl3_paged_attention")
+
+    def __init__(self):
+        for name in self.NAMES:
+            setattr(self, name[len("exl3_"):], self._checked(name))
+
+    @staticmethod
+    def _checked(name):
+        call = getattr(lib, name)
+        types = tuple(call.argtypes)
+
+        def checked(*args):
+            if len(args) != len(types):
+                raise TypeError(f"{name}: takes {len(types)} arguments, got {len(args)}")
+            for a, t in zip(args, types):
+                if t is _F:
+                    float(a)
+                elif not isinstance(a, int) and (a is not None or t is not _P):
+                    raise TypeError(f"{name}: expected an integer, got {type(a).__name__}")
+                elif t is _I and not -1 << 31 <= a < 1 << 31:
+                    raise OverflowError("argument does not fit a C int")       # ctypes would cut it off
+            return call(*args)
+        return checked
+
+
 # The same entry points of the same library without ctypes' conversions, which
-# cost a small call up to a quarter of its time (csrc/binding.c).
+# cost a small call up to a quarter of its time (csrc/binding.c).  It is built
+# for one Python; without it the calls go through ctypes.
 try:
     from . import _binding
-except ImportError as e:
-    raise ImportError("_binding.so not built; run `python -m gemm_exl3_gemv_b200.build`") from e
-_binding.bind([ctypes.cast(getattr(lib, _name), _P).value for _name in _binding.NAMES])
+    _binding.bind([ctypes.cast(getattr(lib, _name), _P).value for _name in _binding.NAMES])
+except ImportError:
+    _binding = _CtypesBinding()
 
 
 class Exl3Error(RuntimeError):
