@@ -37,9 +37,11 @@ def _inputs():
         [os.path.join(ROOT, "include", "exl3.h")]
 
 
-# The debug-bounds variant: every product kernel checks the index of each
-# access to the packed words, the workspace and the outputs, records a failed
-# check in the workspace status word and skips the access (no trap).
+# The debug-bounds variant: every product kernel (trellis and 4-bit) checks the
+# index of each access to the packed words, the workspace and the outputs,
+# records a failed check in the workspace status word and skips the access (no
+# trap).  The cache's and the attention's kernels check page and sequence numbers
+# in every build and have no further checks in this one.
 LIB_DEBUG = os.path.join(HERE, "libexl3_debug.so")
 
 

@@ -54,6 +54,7 @@ struct Q4Args {
     int splits;               // CTAs that share a channel block's inputs
     int depth;                // stages of the rings
     unsigned char* ws;
+    long long part_vecs;      // places of 16 bytes for parts of sums in the workspace (for the debug build's checks)
 };
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -205,18 +206,25 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
     const uint32_t x_to = smem_u32(x_ring) + x_row * S::kXRow + 16 * x_col;
     const long long x_next = (long long)x_rows * p.k_in;
     int fetched = s0;                                        // steps
+    uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
+    const long long scales_all = (long long)(p.k_in / GROUP) * p.n_out;          // and zero points
     auto fetch = [&](int stage) {
         const uint32_t to = smem_u32(ring) + stage * S::kStage;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
 #pragma unroll
             for (int i = 0; i < 2 * SPS; ++i)
-                if (2 * fetched + i < kt_end) copy16(to + c * (SPS * 1024) + i * 512 + lane * 16, words[c] + i * 32);
+                if (2 * fetched + i < kt_end &&
+                    guard(words[c] + i * 32 - reinterpret_cast<const uint4*>(p.packed) < (long long)tn_all * kt_all * 32, status))
+                    copy16(to + c * (SPS * 1024) + i * 512 + lane * 16, words[c] + i * 32);
             words[c] += SPS * 64;
         }
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
-            if (piece_group[j] < group_end) copy16(to + piece_to[j], piece[j]);
+            if (piece_group[j] < group_end &&
+                guard(piece_step[j] == SPS * kParts * p.n_out ? piece[j] - p.zero + 16 <= scales_all
+                                                              : piece[j] - reinterpret_cast<const unsigned char*>(p.scale) + 16 <= 2 * scales_all, status))
+                copy16(to + piece_to[j], piece[j]);
             piece[j] += piece_step[j];
             piece_group[j] += SPS * kParts;
         }
@@ -225,7 +233,8 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
             if (128 * fetched + 8 * (x_col + col) >= 64 * kt_end) break;
             const uint16_t* src = x_from + 8 * col;
             uint32_t dst = xt + 16 * col;
-            for (int row = x_row; row < p.m; row += x_rows, src += x_next, dst += x_rows * S::kXRow) copy16(dst, src);
+            for (int row = x_row; row < p.m; row += x_rows, src += x_next, dst += x_rows * S::kXRow)
+                if (guard(src - p.x + 8 <= (long long)p.m * p.k_in, status)) copy16(dst, src);
         }
         x_from += SPS * 128;
         fetched += SPS;
@@ -349,8 +358,9 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
             const float4 o = red4[v * (S::kRows * row_vecs) + i];
             s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
         }
-        if (p.splits > 1) __stcg(part4 + (size_t)blockIdx.y * vecs + i, s);
-        else red4[i] = s;
+        if (p.splits == 1) red4[i] = s;
+        else if (guard(((long long)blockIdx.x * p.splits + blockIdx.y) * vecs + i < p.part_vecs, status))
+            __stcg(part4 + (size_t)blockIdx.y * vecs + i, s);
     }
     if (p.splits > 1) {
         __threadfence();
@@ -380,6 +390,7 @@ __global__ void __launch_bounds__(256, (Q4Shape<CT, NT, SPS, GROUP>::kMinCtas)) 
             s = red4[i];                                     // written by this thread
         }
         const long long out = (long long)row * p.n_out + (long long)blockIdx.x * ch_cta + ch;
+        if (!guard(out + 4 <= (long long)p.m * p.n_out, status)) continue;
         if (p.y_fp32) {
             *reinterpret_cast<float4*>(static_cast<float*>(p.y) + out) = s;
         } else {
@@ -508,7 +519,8 @@ cudaError_t launch_q4_gemm(int m, const uint16_t* x, const uint32_t* packed, con
 {
     if (takes_tc(m, group)) return launch_q4_tc(m, x, packed, scale, zero, y, y_fp32, k_in, n_out, group, ws, stream);
     const Q4Plan pl = q4_plan(m, k_in, n_out);
-    const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws};
+    const Q4Args a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.warps_c, pl.splits, 0, ws,
+                      (long long)(q4_workspace_need(m, k_in, n_out, group) - ws_data_off()) / 16};
     switch (pl.shape) {
         case 0: return launch_q4_g<0, 1, 1, 4>(a, pl, group, stream);
         case 1: return launch_q4_g<1, 2, 1, 2>(a, pl, group, stream);

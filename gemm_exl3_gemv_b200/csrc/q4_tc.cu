@@ -56,6 +56,7 @@ struct Q4TcArgs {
     int splits;
     unsigned char* ws;
     const unsigned char* xt;  // x as the stages want it, in the workspace
+    size_t xt_bytes;
 };
 
 // Warps: two sets of eight decoders, of four scalers and of one that issues MMAs
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base;
-    Patience wait = {reinterpret_cast<uint32_t*>(p.ws), true};
+    uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
+    Patience wait = {status, true};
 
     if (warp < kFirstScaler) {
         // ------------------------------------------------------ decoders ---
@@ -221,8 +223,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         const uint32_t own = smem_u32(own_all) + warp * (S::kOwnRing * S::kWords) + lane * 16;
         const uint4* words = reinterpret_cast<const uint4*>(p.packed) + ((long long)tn * kt_all + 2 * first) * 32 + lane;
         auto fetch = [&](int stage, int ahead, uint32_t to) {      // `ahead`: of the set's stages, from words on
-            if (stage < s1) copy16(to, words + ahead * (64 * kSets));
-            if (stage < s1 && stage < s_whole) copy16(to + 512, words + ahead * (64 * kSets) + 32);
+            const uint4* from = words + ahead * (64 * kSets);
+            const auto in = [&](const uint4* w) {
+                return guard(w - reinterpret_cast<const uint4*>(p.packed) < (long long)tn_all * kt_all * 32, status);
+            };
+            if (stage < s1 && in(from)) copy16(to, from);
+            if (stage < s1 && stage < s_whole && in(from + 32)) copy16(to + 512, from + 32);
             copies_commit();
         };
         // Zero points: a copy of the warp brings 16 bytes of 32 groups, one such chunk ahead.
@@ -233,7 +239,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         const uint8_t* zeros = p.zero ? p.zero + (long long)z_group * p.n_out + 16 * tn : nullptr;
         auto fetch_zeros = [&](int chunk) {
             if (p.zero) {
-                if (z_group < z_end) copy16(zero_ring + (chunk & 1) * 512 + 16 * lane, zeros);
+                if (z_group < z_end && guard(zeros - p.zero + 16 <= (long long)(p.k_in / GROUP) * p.n_out, status))
+                    copy16(zero_ring + (chunk & 1) * 512 + 16 * lane, zeros);
                 z_group += 32 * kSets;
                 zeros += (long long)(32 * kSets) * p.n_out;
             }
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         int issued = 0;
         for (int s = s0; s < s1 && issued < most; ++s, ++issued) {
             wait.wait(done + slot.at, slot.phase ^ 1);
-            if (!wait.alive) break;
+            if (!wait.alive || !guard((size_t)(s + 1) * kXStage<N> <= p.xt_bytes, status)) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(full + slot.at, kXStage<N>);
                 bulk_g2s(smem + slot.at * kXStage<N>, p.xt + (size_t)s * kXStage<N>, kXStage<N>, full + slot.at);
@@ -321,7 +328,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         const bool brings = ch0 + 8 * (lane & 3) < p.n_out;
         uint32_t f_at = 0;
         auto fetch = [&] {
-            if (brings && f_stage < s1 && f_stage * kParts + f_part < groups) copy16(ring + f_at + 16 * lane, from);
+            if (brings && f_stage < s1 && f_stage * kParts + f_part < groups &&
+                guard(from - p.scale + 8 <= (long long)groups * p.n_out, status))
+                copy16(ring + f_at + 16 * lane, from);
             copies_commit();
             from += (long long)(kSets * 8) * p.n_out;
             f_stage += kSets * kStagesOf8;
@@ -394,7 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         } else if (ch < p.n_out) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (i < p.m) {
+                if (i < p.m && guard((long long)i * p.n_out + ch < (long long)p.m * p.n_out, status)) {
                     if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = y[i];
                     else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(y[i]);
                 }
@@ -451,6 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
             }
             if (ch >= p.n_out) continue;
             const long long to = (long long)row * p.n_out + ch;
+            if (!guard(to + 4 <= (long long)p.m * p.n_out, status)) continue;
             if (p.y_fp32) {
                 *reinterpret_cast<float4*>(static_cast<float*>(p.y) + to) = sum;
             } else {
@@ -467,7 +477,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
 // the packed layout holds.  A thread writes 16 bytes, two pieces of four inputs;
 // rows past the last one are zero.
 template <int N>
-__global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* x, int m, int k_in, unsigned char* xt)
+__global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* x, int m, int k_in, unsigned char* xt, size_t xt_bytes,
+                                                   uint32_t* status)
 {
     grid_dep_wait();
     grid_dep_launch();                                       // behind the wait: the product may then read its weights at once
@@ -475,12 +486,13 @@ __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* x, int m, int
     if (half >= k_in / 64) return;
     const int k = 64 * half + 32 * (chunk >> 2) + 4 * ((chunk >> 1) & 1) + 16 * (chunk & 1);
     uint2 lo = make_uint2(0, 0), hi = lo;
-    if (row < m) {
+    if (row < m && guard((long long)row * k_in + k + 12 <= (long long)m * k_in, status)) {
         const uint2* from = reinterpret_cast<const uint2*>(x + (long long)row * k_in + k);
         lo = from[0];
         hi = from[2];
     }
-    *reinterpret_cast<uint4*>(xt + (size_t)half * (N * 128) + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    const size_t to = (size_t)half * (N * 128) + row * 128 + ((chunk ^ (row & 7)) << 4);
+    if (guard(to + 16 <= xt_bytes, status)) *reinterpret_cast<uint4*>(xt + to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
 template <int N, int GROUP>
@@ -494,7 +506,7 @@ cudaError_t launch_t(const Q4TcArgs& a, int blocks, cudaStream_t stream)
     });
     if (e != cudaSuccess) return e;
     const cudaError_t ex = launch_pdl(q4_x_kernel<N>, dim3((unsigned)((a.k_in / 64 * 8 * N + 255) / 256)), dim3(256), 0, stream, a.x,
-                                      a.m, a.k_in, const_cast<unsigned char*>(a.xt));
+                                      a.m, a.k_in, const_cast<unsigned char*>(a.xt), a.xt_bytes, reinterpret_cast<uint32_t*>(a.ws));
     if (ex != cudaSuccess) return ex;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -537,7 +549,8 @@ cudaError_t launch_q4_tc(int m, const uint16_t* x, const uint32_t* packed, const
                          void* y, int y_fp32, int k_in, int n_out, int group, unsigned char* ws, cudaStream_t stream)
 {
     const Q4TcPlan pl = q4_tc_plan(k_in, n_out);
-    const Q4TcArgs a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws, ws + ws_data_off()};
+    const Q4TcArgs a = {x, packed, scale, zero, y, m, k_in, n_out, y_fp32 ? 1 : 0, pl.splits, ws, ws + ws_data_off(),
+                        pl.x_bytes(m, k_in)};
     if (m <= 16) return group == 64 ? launch_t<16, 64>(a, pl.blocks, stream) : launch_t<16, 128>(a, pl.blocks, stream);
     return group == 32 ? launch_t<32, 32>(a, pl.blocks, stream)
                        : group == 64 ? launch_t<32, 64>(a, pl.blocks, stream) : launch_t<32, 128>(a, pl.blocks, stream);
