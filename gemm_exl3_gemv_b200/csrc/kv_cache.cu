@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int 
     const int old_fault = __ldcg(a.scratch + kKvFault);
     __syncthreads();
     bool bad = false;
-    for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, seqs[e], a.n_seqs) || (counts && counts[e] > m);
+    for (int e = threadIdx.x; e < n; e += blockDim.x) bad |= !mark(seen, seqs[e], a.n_seqs) || (counts && (counts[e] < 0 || counts[e] > m));
     if (__syncthreads_or(bad)) {
         if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) fault(a, kKvIndex);
         return;

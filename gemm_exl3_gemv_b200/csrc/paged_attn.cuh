@@ -94,16 +94,16 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, const AttnPlan& pl,
 {
     Entry r;
     const int b = e / pl.row_tiles, rt = e % pl.row_tiles;
-    const int c = a.counts ? min(max(a.counts[b], 0), a.m) : a.m;
+    int c = a.counts ? a.counts[b] : a.m;
     r.seq = a.seqs[b];
+    if (r.seq < 0 || r.seq >= a.c.n_seqs || c < 0 || c > a.m) {
+        atomicOr(a.c.scratch + kKvFault, kKvIndex);
+        c = 0;
+    }
     r.count = c;
     r.row0 = rt * pl.tile_rows;
     r.rows = min(c * a.group - r.row0, pl.tile_rows);
     r.sink_tiles = r.tile0 = r.tiles = r.len = 0;
-    if (r.seq < 0 || r.seq >= a.c.n_seqs) {
-        atomicOr(a.c.scratch + kKvFault, kKvIndex);
-        r.rows = 0;
-    }
     if (r.rows <= 0) { r.rows = 0; return r; }
     r.len = min(max(a.c.lens[r.seq], 0), a.c.max_pages << pl.page_shift);
     const int p0 = r.len - c + r.row0 / a.group, p1 = r.len - c + (r.row0 + r.rows - 1) / a.group;

@@ -167,7 +167,9 @@ class KvCache:
     def write(self, layer: int, seqs: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               counts: Optional[torch.Tensor] = None, stream=None):
         """Keys and values (n, m, n_heads, head_dim) of the last m (counts:
-        counts[b]) tokens of each sequence, in one layer."""
+        counts[b]) tokens of each sequence, those that ``extend`` made room
+        for, in one layer.  (A page that several sequences hold is written for
+        all of them.)"""
         n = self._entries(seqs, "seqs")
         p, c = self._list(seqs, "seqs", n), self._list(counts, "counts", n)
         m, bs, rs = self._rows(k, "k", n, self.n_heads)
@@ -229,7 +231,7 @@ class KvCache:
         and the first ``sinks`` of the sequence.  scale: 1/sqrt(head_dim) by
         default.  lse: (n, m, n_q_heads) fp32, filled with the logarithms of
         the softmax sums.  Rows from counts[b] on are left as they were (in an
-        ``out`` made here: zero)."""
+        ``out`` made here: zero).  ``out`` may be ``q``."""
         if stream is not None and (out is None or workspace is None):
             with torch.cuda.stream(stream):             # what is allocated here belongs to the stream that uses it
                 return self.attention(layer, seqs, q, counts, scale, window, sinks, out, lse, workspace)

@@ -378,7 +378,7 @@ EXL3_API int exl3_q4_pack(const uint8_t *q, int k_in, int n_out, uint32_t *packe
  * device: a number out of range or a repeated one makes the whole call do
  * nothing and is reported by exl3_kv_status as EXL3_ERR_INDEX.
  * (exl3_paged_attention, which changes nothing, answers a repeated number twice
- * and leaves out the rows of a bad one.)
+ * and leaves out the rows of a bad one, or of a bad count.)
  */
 typedef struct exl3_kv_cache {
     uint16_t *k;
@@ -426,7 +426,9 @@ EXL3_API int exl3_kv_extend(const exl3_kv_cache_t *cache, int n, int m, const in
  * counts[b] tokens of seqs[b], after the exl3_kv_extend with the same list.
  *   k_new, v_new : row i of entry b at element b*batch_stride + i*row_stride,
  *                  n_heads x head_dim fp16 each; strides multiples of 8.
- * Rows i >= counts[b] are not read.
+ * Rows i >= counts[b] are not read.  A count outside 0..m makes the call do
+ * nothing (EXL3_ERR_INDEX).  A page that several sequences hold is written for
+ * all of them (of the tokens that the extend brought none lies on one).
  */
 EXL3_API int exl3_kv_write(const exl3_kv_cache_t *cache, int layer, int n, int m, const int32_t *seqs,
                            const int32_t *counts, const uint16_t *k_new, const uint16_t *v_new,
@@ -481,7 +483,8 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  * on the lengths alone: repeated calls are bitwise identical.
  * A table entry out of range is not followed: exl3_kv_status then reports
  * EXL3_ERR_INDEX, and the rows that needed it are not valid; the same for a
- * bad number in seqs, whose rows are left as they were.  Bounded waits as in
+ * bad number in seqs or a count outside 0..m, whose rows are left as they were.
+ * out may be q itself (the same strides).  Bounded waits as in
  * exl3_gemm_small_m (exl3_workspace_status; a nonzero injection word, low byte
  * v, lets a CTA's first v - 1 tiles through).  After EXL3_ERR_TIMEOUT, zero-fill
  * the workspace before its next use: parts of a cut sequence may have been
