@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional
 
@@ -147,14 +148,11 @@ class _CtypesBinding:
         def checked(*args):
             if len(args) != len(types):
                 raise TypeError(f"{name}: takes {len(types)} arguments, got {len(args)}")
-            for a, t in zip(args, types):
-                if t is _F:
-                    float(a)
-                elif not isinstance(a, int) and (a is not None or t is not _P):
-                    raise TypeError(f"{name}: expected an integer, got {type(a).__name__}")
-                elif t is _I and not -1 << 31 <= a < 1 << 31:
+            values = [a if a is None and t is _P else float(a) if t is _F else operator.index(a) for a, t in zip(args, types)]
+            for a, t in zip(values, types):
+                if t is _I and not -1 << 31 <= a < 1 << 31:
                     raise OverflowError("argument does not fit a C int")       # ctypes would cut it off
-            return call(*args)
+            return call(*values)
         return checked
 
 

@@ -53,3 +53,23 @@ sys.exit(pytest.main(["-q", "-x", "-p", "no:cacheprovider", "tests/test_gpu_deco
                       "serving or one_row or strided or truncate or compact or default or stack"]))
 """)
     assert out.returncode == 0, out.stdout[-3000:] + out.stderr[-2000:]
+
+
+def test_both_forms_take_numbers_of_other_kinds():
+    """NumPy's whole numbers as Python's; a number with a fraction is none."""
+    code = """
+import numpy as np
+from gemm_exl3_gemv_b200 import exl3 as ex
+b = ex._binding
+assert b.kv_extend(None, np.int64(1), np.int32(1), 17, None, 0) == ex.EXL3_ERR_INVALID_ARG
+for args in ((None, 1.0, 1, 17, None, 0), (None, 1, 1, "17", None, 0), (None, None, 1, 17, None, 0)):
+    try:
+        b.kv_extend(*args)
+    except TypeError:
+        continue
+    raise AssertionError(args)
+print(type(b).__name__)
+"""
+    for first, kind in (("", "module"), (HIDE, "_CtypesBinding")):
+        out = run(first + code)
+        assert out.returncode == 0 and out.stdout.strip() == kind, out.stdout + out.stderr
