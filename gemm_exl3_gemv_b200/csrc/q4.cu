@@ -437,9 +437,10 @@ constexpr int least_warps_c(int shape) { return shape == 0 ? 1 : shape == 1 ? 2 
 // Whether the other kernel takes the product.  It decodes faster and needs no
 // more for 32 rows than for 9, but takes a launch more, 16 rows at least, and
 // has a sum per group to read and scale.  This kernel against it, groups of 128:
-// 8 rows of 5120 x 5120 9.0 and 10.5 us, 12 rows 11.6 and 10.6, 32 rows 17.4 and
-// 11.4; 12 rows of 2048 x 2048 6.8 and 6.3.  Groups of 32: 16 rows of 17408 x
-// 5120 23.0 and 27.6 us, 24 rows 28.4 and 32.8, 32 rows 37.1 and 32.5.
+// 8 rows of 5120 x 5120 8.4 and 9.4 us, 12 rows 10.8 and 9.4, 32 rows 17.0 and
+// 10.3; 12 rows of 2048 x 2048 6.8 and 6.5.  Groups of 32: 16 rows of 17408 x
+// 5120 22.5 and 26.2 us, 24 rows 27.7 and 31.6, 32 rows 36.3 and 31.7 (of small
+// matrices the other is ahead earlier: 24 rows of 2048 x 2048 8.9 and 7.7).
 bool takes_tc(int m, int group) { return m > (group == 32 ? 24 : 8); }
 
 Q4Plan q4_plan(int m, int k_in, int n_out)

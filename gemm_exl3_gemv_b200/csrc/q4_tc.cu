@@ -28,8 +28,8 @@
 // about 5 us for the launches, the first bytes and the end.  Two sets of warps
 // take stages in turn, so that one stage's waits are another's work: a wait on a
 // barrier costs 150 clocks even if its phase is over.  32 rows of 5120 x 17408 in
-// groups of 128 take 18.8 us (2.6 TB/s; on the legacy tensor pipe 29.9), 16 rows
-// 17.1 (19.9), 32 rows of 5120 x 5120 11.0 (17.3).
+// groups of 128 take 18.5 us (2.6 TB/s; on the legacy tensor pipe 29.3), 16 rows
+// 16.9 (19.6), 32 rows of 5120 x 5120 10.3 (17.0).
 // CTAs that split the inputs of a block of channels are a cluster; they add up
 // their parts, in order, through each other's shared memory (through memory and
 // the last one to arrive: 15.0 us for 5120 x 5120).
@@ -382,8 +382,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
             d.template next<kSets>();
         }
         copies_wait<0>();
-        // the sets' sums
-        // (through the ring of the second set's decoders, whose last stage is done)
+        // the sets' sums, through the ring of the second set's decoders, whose last stage is done
         float* mine = reinterpret_cast<float*>(own_all + S::kOwnAll / 2) + 32 * quarter + lane;
         static_assert(N * 128 * 4 <= S::kOwnAll / 2);
         if (set == 1) {
@@ -392,22 +391,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) q4_tc_kernel(const __grid_const
         }
         named_bar(2, 32 * kSets * kScalers);
         if (set == 0) {
-        float y[N];
+            float y[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) + mine[i * 128];
-        // ---- the result, or a part of it ----
-        if (p.splits > 1) {
-            float* part = reinterpret_cast<float*>(own_all) + 32 * quarter + lane;           // where the first set's decoders had their ring
+            for (int i = 0; i < N; ++i) y[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) + mine[i * 128];
+            // ---- the result, or a part of it ----
+            if (p.splits > 1) {
+                float* part = reinterpret_cast<float*>(own_all) + 32 * quarter + lane;       // where the first set's decoders had their ring
 #pragma unroll
-            for (int i = 0; i < N; ++i) part[i * 128] = y[i];
-        } else if (ch < p.n_out) {
+                for (int i = 0; i < N; ++i) part[i * 128] = y[i];
+            } else if (ch < p.n_out) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < p.m && guard((long long)i * p.n_out + ch < (long long)p.m * p.n_out, status)) {
-                    if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = y[i];
-                    else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(y[i]);
-                }
-        }
+                for (int i = 0; i < N; ++i)
+                    if (i < p.m && guard((long long)i * p.n_out + ch < (long long)p.m * p.n_out, status)) {
+                        if (p.y_fp32) static_cast<float*>(p.y)[(long long)i * p.n_out + ch] = y[i];
+                        else static_cast<__half*>(p.y)[(long long)i * p.n_out + ch] = __float2half_rn(y[i]);
+                    }
+            }
         }
     } else {
         // ----------------------------------------------------- MMA warps ---

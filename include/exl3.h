@@ -318,9 +318,10 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  *   group  : 32, 64 or 128.   k_in : positive multiple of 64 and of group, at
  *            most 2^20.   n_out : positive multiple of 16, at most 1,048,576.
  *   workspace, ws_bytes : at least exl3_q4_workspace_bytes(m, k_in, n_out)
- *            bytes (which is enough for fewer rows too), 256-byte aligned, zero-filled before first use; shared by
- *            calls on one stream as described at exl3_workspace_bytes (it may
- *            be the same buffer as the trellis products').
+ *            bytes (which is enough for fewer rows too), 256-byte aligned,
+ *            zero-filled before first use; shared by calls on one stream as
+ *            described at exl3_workspace_bytes (it may be the same buffer as the
+ *            trellis products').
  * Layout of packed: tiles of 16 channels x 64 inputs, tile (tn, tk) at
  *   (tn*(k_in/64) + tk)*128 uint32 words; word 4*(4*g + t) + j of a tile
  *   (g < 8, t < 4, j < 4) holds channels 16*tn + g + 8*c, c < 2, and inputs
@@ -330,9 +331,10 @@ EXL3_API int exl3_gemv_noalloc(const uint16_t *x, const uint32_t *packed, const 
  * summed in fp32, and each group's sum is scaled in fp32.  The order of every
  * sum is fixed: repeated calls are bitwise identical.  An infinity or NaN in a
  * row of x makes outputs of that row what the definition gives (infinite, or
- * NaN where q = zero), and touches no other row.  Timeouts, where m > 8: as in
- * exl3_gemm_small_m (reported by exl3_workspace_status alone; a nonzero
- * injection word, low byte v, lets a CTA's first v - 1 stages of x through).
+ * NaN where q = zero), and touches no other row.  Timeouts, where m > 8 (in
+ * groups of 32: m > 24): as in exl3_gemm_small_m (reported by
+ * exl3_workspace_status alone; a nonzero injection word, low byte v, lets a
+ * CTA's first v - 1 stages of x through).
  */
 EXL3_API size_t exl3_q4_workspace_bytes(int m, int k_in, int n_out);
 EXL3_API int exl3_q4_gemm(int m, const uint16_t *x, const uint32_t *packed, const uint16_t *scale,
@@ -470,8 +472,10 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  *   q    : row i of entry b at element b*q_batch_stride + i*q_row_stride,
  *          n_q_heads x head_dim fp16.   n_q_heads : a multiple of n_heads, at
  *          most 32 of them per head of the cache.
- *   out  : as q, with its own strides, whose rows must not overlap.   lse : n x m x n_q_heads fp32, the
- *          natural logarithm of each softmax's sum of exponentials; or NULL.
+ *   out  : as q, with its own strides, whose rows must not overlap; it may be q
+ *          itself, with the same strides.
+ *   lse  : n x m x n_q_heads fp32, the natural logarithm of each softmax's sum
+ *          of exponentials; or NULL.
  *   scale: finite.   window, sinks : >= 0.
  *   workspace, ws_bytes : at least exl3_paged_attention_workspace_bytes(...)
  *          bytes, 256-byte aligned, zero-filled before first use, shared by
@@ -479,16 +483,19 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  * Rows i >= counts[b] of out and lse are left as they were.  A row that sees
  * no token gets zeros (lse -inf).  Keys and values that a row does not see
  * have no influence on it, whatever they hold.  Scores, the softmax's
- * statistics and the weighted sums are fp32.  The order of every sum depends
- * on the lengths alone: repeated calls are bitwise identical.
+ * statistics and the weighted sums are fp32; probabilities are rounded to fp16
+ * as operands of the second product, by at most 2^-11 of themselves.  The order
+ * of every sum is fixed for a call: the same lengths, counts, order of the list,
+ * window, sinks, numbers of rows and heads, page size and max_pages give the same
+ * bits.  The same sequence in another batch, or in a wider table, may be cut and
+ * joined elsewhere and differ in the last bits.
  * A table entry out of range is not followed: exl3_kv_status then reports
  * EXL3_ERR_INDEX, and the rows that needed it are not valid; the same for a
  * bad number in seqs or a count outside 0..m, whose rows are left as they were.
- * out may be q itself (the same strides).  Bounded waits as in
- * exl3_gemm_small_m (exl3_workspace_status; a nonzero injection word, low byte
- * v, lets a CTA's first v - 1 tiles through).  After EXL3_ERR_TIMEOUT, zero-fill
- * the workspace before its next use: parts of a cut sequence may have been
- * counted and not joined.
+ * Bounded waits as in exl3_gemm_small_m (exl3_workspace_status; a nonzero
+ * injection word, low byte v, lets a CTA's first v - 1 tiles through).  After
+ * EXL3_ERR_TIMEOUT, zero-fill the workspace before its next use: parts of a cut
+ * sequence may have been counted and not joined.
  */
 EXL3_API size_t exl3_paged_attention_workspace_bytes(int m, int n_q_heads, int n_heads, int head_dim);
 /* Kernel launches of one call (0 for an invalid one).  Host-only. */
