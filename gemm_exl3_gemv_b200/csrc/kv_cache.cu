@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kExtThreads) kv_extend_kernel(KvArgs a, int n,
 // loads) is shared by the pieces of a row through the L1.  Every CTA checks the
 // whole list first, as a repeated sequence would be written by two entries in
 // no order.  Bound by memory: 2001 tokens of two sequences, 8 heads of 128, take
-// 7.4 us (4.4 TB/s); of one token of 64 sequences, 2.3 us, the launch and the
-// chain of reads.
+// 7.2 us (4.6 TB/s), 2665 in all 5.8 (3.7); of one token of 64 sequences, 2.4 us,
+// the launch and the chain of reads.
 
 __global__ void __launch_bounds__(256) kv_write_kernel(KvArgs a, int layer, int n, int m, const int* seqs, const int* counts,
                                                        const uint16_t* k_new, const uint16_t* v_new, long long bs,

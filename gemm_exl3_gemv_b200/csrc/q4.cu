@@ -9,7 +9,7 @@
 // bound, if a weight costs less than about three instruction slots (148 SMs x
 // 128 lanes at 1.9 GHz against 13e12 weights a second).  Measured, the words'
 // and scales' bytes over the time: one row of 5120 x 17408 in groups of 128,
-// 13.8 us (3.4 TB/s), of 4096 x 4096 5.2 us, where a launch and the first bytes,
+// 13.1 us (3.6 TB/s), of 4096 x 4096 4.3 us, where a launch and the first bytes,
 // about 3 us, are the larger part.
 //   * The packed tiles (16 channels x 64 inputs, layout in include/exl3.h) are
 //     the A operand of mma.m16n8k16 in register order: a lane's 128-bit load
@@ -448,7 +448,7 @@ Q4Plan q4_plan(int m, int k_in, int n_out)
     Q4Plan pl;
     // Up to 2 rows warps of 16 channels have the deeper stages, and pay where a CTA
     // per 16 channels, whose warps split the inputs, finds a place at once: one row
-    // of 4096 x 4096 5.2 us, warps of 32 channels 7.1; of 17408 x 5120 21.9, 17.1.
+    // of 4096 x 4096 4.3 us, warps of 32 channels 6.5; of 17408 x 5120 19.9, 16.0.
     pl.shape = m <= 2 && n_out / 16 <= 148 * 2 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : 3;
     pl.ct = pl.shape == 0 ? 1 : 2;
     const int steps = (k_in / 64 + 1) / 2, tiles = (n_out / 16 + pl.ct - 1) / pl.ct;
