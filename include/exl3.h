@@ -476,7 +476,8 @@ EXL3_API int exl3_kv_compact(const exl3_kv_cache_t *cache, void *stream);
  *          itself, with the same strides.
  *   lse  : n x m x n_q_heads fp32, the natural logarithm of each softmax's sum
  *          of exponentials; or NULL.
- *   scale: finite.   window, sinks : >= 0.
+ *   scale: finite, and so small that scaled scores are finite in fp32.
+ *   window, sinks : >= 0.
  *   workspace, ws_bytes : at least exl3_paged_attention_workspace_bytes(...)
  *          bytes, 256-byte aligned, zero-filled before first use, shared by
  *          calls on one stream.
